@@ -10,6 +10,7 @@ Layouts (BHSD, contiguous): q, o, dout, dq [B, Hq, Nq, d]; k, v, dk, dv
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -99,6 +100,16 @@ def lib() -> ctypes.CDLL:
             L.fa_selftest_wait_timeout.restype = ip
             L.fa_testhook_tile_slot.argtypes = [ip, uip]
             L.fa_testhook_tile_slot.restype = ip
+            L.fa_fwd_window.argtypes = [ip, vp, vp, vp, vp, vp, ip, ip, ip, ip, ip, ip, fl, ip, ip, vp]
+            L.fa_fwd_window.restype = ip
+            L.fa_bwd_window_workspace_size.argtypes = [ip] * 8
+            L.fa_bwd_window_workspace_size.restype = sz
+            L.fa_bwd_window.argtypes = [ip] + [vp] * 9 + [ip] * 6 + [fl, ip, ip, vp, sz, vp]
+            L.fa_bwd_window.restype = ip
+            L.fa_fwd_paged_window_workspace_size.argtypes = [ip] * 10
+            L.fa_fwd_paged_window_workspace_size.restype = sz
+            L.fa_fwd_paged_window.argtypes = [ip] + [vp] * 7 + [ip] * 8 + [fl, ip, ip, ip, vp, sz, vp]
+            L.fa_fwd_paged_window.restype = ip
             _lib = L
         return _lib
 
@@ -375,6 +386,124 @@ def fa_bwd(q, k, v, o, dout, lse, dq=None, dk=None, dv=None, *, causal=False, sc
                                _ptr(dq), _ptr(dk), _ptr(dv), B, Hq, Hkv, Nq, Nk, d, scale,
                                int(bool(causal)), _ptr(workspace), ws_bytes, _stream(stream)))
     return dq, dk, dv
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _on_device(stream, q, **others):
+    """A context in which q's device (and `stream`, if given) is current, so that outputs are
+    allocated and kernels launched there; every other tensor must be on q's device."""
+    import torch
+    if not q.is_cuda:
+        raise ValueError("q must be a contiguous CUDA tensor")
+    for name, t in others.items():
+        if t is not None and t.device != q.device:
+            raise ValueError(f"{name} is on {t.device}, q on {q.device}")
+    if stream is not None:
+        if stream.device != q.device:
+            raise ValueError(f"stream is of {stream.device}, q on {q.device}")
+        return torch.cuda.stream(stream)
+    if q.device.index != torch.cuda.current_device():
+        return torch.cuda.device(q.device)
+    return _NO_CONTEXT
+
+
+def _scale(scale, d):
+    return 1.0 / math.sqrt(d) if scale is None else float(scale)
+
+
+def fa_fwd_window(q, k, v, window, sinks=0, o=None, lse=None, *, scale=None, stream=None, want_lse=True):
+    """Forward with a sliding window and sinks (causal): each query sees the ``window`` newest keys
+    up to its own and the first ``sinks`` keys.  bf16 or fp16; returns (o, lse)."""
+    import torch
+    B, Hq, Hkv, Nq, Nk, d = _dims(q, k)
+    dt = _dtype_code(q)
+    _check_io(q, k, v, o, q.dtype)
+    _require_lse(lse, B, Hq, Nq)
+    with _on_device(stream, q, k=k, v=v, o=o, lse=lse):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+        _check(lib().fa_fwd_window(dt, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Nk, d,
+                                   _scale(scale, d), int(window), int(sinks), _stream(None)))
+    return o, lse
+
+
+def fa_bwd_window_workspace_size(B, Hq, Hkv, Nq, Nk, d, window, sinks=0) -> int:
+    return int(lib().fa_bwd_window_workspace_size(B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks)))
+
+
+def fa_bwd_window(q, k, v, o, dout, lse, window, sinks=0, dq=None, dk=None, dv=None, *, scale=None,
+                  workspace=None, stream=None):
+    """Backward of ``fa_fwd_window``: returns (dq, dk, dv).  Allocates the gradients when not given."""
+    import torch
+    B, Hq, Hkv, Nq, Nk, d = _dims(q, k)
+    dt = _dtype_code(q)
+    _check_io(q, k, v, o, q.dtype)
+    _require(dout, "dout", q.dtype, q.shape)
+    _require(lse, "lse", torch.float32, (B, Hq, Nq))
+    for t, n, ref in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
+        if t is not None:
+            _require(t, n, q.dtype, ref.shape)
+    ws_bytes = _ws_bytes(workspace)
+    with _on_device(stream, q, k=k, v=v, o=o, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv, workspace=workspace):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        _check(lib().fa_bwd_window(dt, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
+                                   _ptr(dk), _ptr(dv), B, Hq, Hkv, Nq, Nk, d, _scale(scale, d), int(window),
+                                   int(sinks), _ptr(workspace), ws_bytes, _stream(None)))
+    return dq, dk, dv
+
+
+def _paged_args(q, k_cache, v_cache, block_table, seq_lens, o, lse):
+    """Checked (dtype code, B, Hq, Hkv, Nq, d, page_size, num_pages, max_pages) of a paged call."""
+    import torch
+    B, Hq, Nq, d = q.shape
+    num_pages, page_size, Hkv, dk = k_cache.shape
+    if dk != d or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("k_cache / v_cache shapes disagree with q")
+    dt = _dtype_code(q)
+    _require(q, "q", q.dtype)
+    _require(k_cache, "k_cache", q.dtype)
+    _require(v_cache, "v_cache", q.dtype)
+    _require(block_table, "block_table", torch.int32)
+    _require(seq_lens, "seq_lens", torch.int32, (B,))
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages_per_seq]")
+    if o is not None:
+        _require(o, "o", q.dtype, q.shape)
+    _require_lse(lse, B, Hq, Nq)
+    return dt, B, Hq, Hkv, Nq, d, page_size, num_pages, block_table.shape[1]
+
+
+def fa_fwd_paged_window_workspace_size(B, Hq, Hkv, Nq, page_size, max_pages_per_seq, d, window, sinks=0,
+                                       num_splits=0) -> int:
+    return int(lib().fa_fwd_paged_window_workspace_size(B, Hq, Hkv, Nq, page_size, max_pages_per_seq, d,
+                                                        int(window), int(sinks), num_splits))
+
+
+def fa_fwd_paged_window(q, k_cache, v_cache, block_table, seq_lens, window, sinks=0, o=None, lse=None, *,
+                        scale=None, num_splits=0, workspace=None, stream=None):
+    """``fa_fwd_window`` for single tokens (or the last few) over a paged KV cache: arguments as
+    ``fa_fwd_paged``, the window against each sequence's own length."""
+    import torch
+    dt, B, Hq, Hkv, Nq, d, page_size, num_pages, max_pages = _paged_args(q, k_cache, v_cache, block_table,
+                                                                         seq_lens, o, lse)
+    ws_bytes = _ws_bytes(workspace)
+    with _on_device(stream, q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens, o=o,
+                    lse=lse, workspace=workspace):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+        _check(lib().fa_fwd_paged_window(dt, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+                                         _ptr(seq_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, d, page_size,
+                                         num_pages, max_pages, _scale(scale, d), int(window), int(sinks),
+                                         int(num_splits), _ptr(workspace), ws_bytes, _stream(None)))
+    return o, lse
 
 
 def fa_check_device_status(stream=None):

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(BwdParams p)
     const T* po = static_cast<const T*>(p.o);
     const T* pd = static_cast<const T*>(p.dout);
     float s[2] = {0.f, 0.f};
-    if (p.q_split > 1) {
+    if (p.split_cnt) {
         for (int i = (int)(blockIdx.x * blockDim.x + threadIdx.x); i < 2 * p.n_split_units;
              i += (int)(gridDim.x * blockDim.x))
             p.split_cnt[i] = 0;
@@ -280,6 +280,24 @@ __device__ __forceinline__ void bwd_q_range(const BwdParams& p, int kb, int& qb0
     nqb = max(0, nqb_all - qb0);
 }
 
+// The same under a sliding window with sinks: the last query that sees a key j >= sinks is at
+// position j + window - 1; a block that holds sinks is seen by every later query.
+__host__ __device__ __forceinline__ void bwd_win_q_range(int kb, int Nq, int Nk, int window, int sinks, int& qb0,
+                                                         int& nqb)
+{
+    const int nqb_all = (Nq + 63) / 64, delta = Nk - Nq;
+    const int k_end = kb * 128 + 127 < Nk - 1 ? kb * 128 + 127 : Nk - 1;   // last key of the block
+    const int first_row = kb * 128 - delta;
+    qb0 = first_row <= 0 ? 0 : first_row / 64;
+    int end = nqb_all;
+    if (kb * 128 >= sinks) {
+        const int last_row = k_end + window - 1 - delta;
+        end = last_row < 0 ? 0 : last_row / 64 + 1;
+        end = end < nqb_all ? end : nqb_all;
+    }
+    nqb = end > qb0 ? end - qb0 : 0;
+}
+
 // byte offset of (row, 16-byte chunk) in a tile of 128-byte swizzled rows
 __device__ __forceinline__ uint32_t sw128_off(int row, int chunk)
 {
@@ -287,8 +305,10 @@ __device__ __forceinline__ uint32_t sw128_off(int row, int chunk)
 }
 
 // SPLIT: the launch shares units between CTAs (q_split > 1); without it the kernel
-// carries none of the split's code
-template <int D, bool CAUSAL, typename T = __nv_bfloat16, bool SPLIT = false>
+// carries none of the split's code.  WIN: sliding window with sinks; a launch of up to two
+// parts, first the units of the key blocks that hold sinks (sink_split CTAs each), then the
+// others (q_split each)
+template <int D, bool CAUSAL, typename T = __nv_bfloat16, bool SPLIT = false, bool WIN = false>
 __global__ void __launch_bounds__(384, 1)
     bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -327,16 +347,30 @@ __global__ void __launch_bounds__(384, 1)
 
     griddep_launch_dependents();   // bwd_post may take the SMs this launch frees
     const int warp = warp_id(), lane = lane_id();
-    const int nsp = SPLIT ? p.q_split : 1;                         // CTAs per unit
+    static_assert(!WIN || (CAUSAL && SPLIT), "the windowed launch is causal and may be split");
     const int units = p.B * p.Hkv * C::kFeatSplit;                 // units per key block
-    const int kb = (int)blockIdx.x / (units * nsp);   // small key blocks (most work) first
-    const int ui = ((int)blockIdx.x % (units * nsp)) / nsp;
-    const int sp = (int)blockIdx.x % nsp;                          // share of the unit's steps
+    int bid = (int)blockIdx.x, kb_first = 0;
+    int nsp = SPLIT ? p.q_split : 1;                               // CTAs per unit
+    if constexpr (WIN) {
+        const int n_sink = p.sink_blocks * units * p.sink_split;   // CTAs of the sinks' part
+        if (bid < n_sink) {
+            nsp = p.sink_split;
+        } else {
+            bid -= n_sink;
+            kb_first = p.sink_blocks;
+        }
+    }
+    const int kb = kb_first + bid / (units * nsp);   // small key blocks (most work) first
+    const int ui = (bid % (units * nsp)) / nsp;
+    const int sp = bid % nsp;                                      // share of the unit's steps
     const int kvh = ui / C::kFeatSplit;
     const int fh = ui % C::kFeatSplit;   // feature half (head size 256)
     const int b = kvh / p.Hkv, hk = kvh % p.Hkv;
     int qb0, nqb;
-    bwd_q_range(p, kb, qb0, nqb);
+    if constexpr (WIN)
+        bwd_win_q_range(kb, p.Nq, p.Nk, p.window, p.sinks, qb0, nqb);
+    else
+        bwd_q_range(p, kb, qb0, nqb);
     if (!CAUSAL) {
         qb0 = 0;
         nqb = p.Nq_pad / 64;
@@ -601,6 +635,22 @@ __global__ void __launch_bounds__(384, 1)
                 return true;
             };
             bool ok = mbar_wait_w(bar_kv, 0, abort_flag);
+            if constexpr (WIN) {
+                // keys between the sinks and the first query's window are seen by no query: zero
+                // their K and V rows, so that whatever they hold adds nothing (0 * NaN)
+                const int u0 = max(p.sinks - kb * 128, 0), u1 = min(p.Nk - p.Nq - p.window + 1 - kb * 128, 128);
+                if (ok && u0 < u1) {
+                    const int n = (u1 - u0) * 8;   // 16-byte chunks per panel
+                    for (int pn = 0; pn < D / 64; ++pn)
+                        for (int i = lane; i < n; i += 32) {
+                            const int o = pn * C::kKPanel + u0 * 128 + i * 16;
+                            *reinterpret_cast<uint4*>(smem + C::kOffK + o) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4*>(smem + C::kOffV + o) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            }
             if constexpr (C::kHalves) {
             // per step it: S^T / dP^T of step it + 1 over the other half (under step it's
             // exponentials); step it's dV (frees the dO half), dK (frees its Q buffer)
@@ -729,7 +779,9 @@ __global__ void __launch_bounds__(384, 1)
             uint32_t pp[32], dd[32];
             const float2 sl22 = make_float2(sl2, sl2);
             // rows >= min_row see the key; whole 64-row block visible in most steps
-            const bool all_vis = key_ok && (q_first >= min_row);
+            // (and, under a window, rows <= max_row)
+            const int max_row = !WIN || key < p.sinks ? INT_MAX : min_row + p.window - 1;
+            const bool all_vis = key_ok && (q_first >= min_row) && (!WIN || q_first + 63 <= max_row);
 #pragma unroll
             for (int c4 = 0; c4 < 16; ++c4) {
                 const float4 nl4 = nlse4[c4], nd4 = ndlt4[c4];
@@ -742,8 +794,8 @@ __global__ void __launch_bounds__(384, 1)
                         ffma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl22, nl);
                     float2 pv = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                     if (!all_vis) {
-                        pv.x = (key_ok && q_first + c >= min_row) ? pv.x : 0.f;
-                        pv.y = (key_ok && q_first + c + 1 >= min_row) ? pv.y : 0.f;
+                        pv.x = (key_ok && q_first + c >= min_row && (!WIN || q_first + c <= max_row)) ? pv.x : 0.f;
+                        pv.y = (key_ok && q_first + c + 1 >= min_row && (!WIN || q_first + c + 1 <= max_row)) ? pv.y : 0.f;
                     }
                     // dS = P * (dP - D)
                     const float2 dd2 = fadd2(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), nd);
@@ -787,7 +839,19 @@ __global__ void __launch_bounds__(384, 1)
         }
         int ticket = nsp - 1;   // the last CTA of the unit (the only one without a split)
         // the unit's counters, from the block index again (nothing kept live over the steps)
-        const int unit_e = SPLIT ? (int)(ctaid_x() / (uint32_t)nsp) : 0;
+        int unit_e = SPLIT ? (int)(ctaid_x() / (uint32_t)nsp) : 0;
+        int cta_e = SPLIT ? (int)ctaid_x() : 0;   // index within the launch's part
+        size_t slot_e = 0;                        // first partial slot of the part's units, less unit_e's share
+        if constexpr (WIN) {
+            const int part_units = p.sink_blocks * p.B * p.Hkv * C::kFeatSplit, n_sink = part_units * p.sink_split;
+            if (cta_e >= n_sink) {
+                cta_e -= n_sink;
+                unit_e = part_units + cta_e / nsp;
+                // the sinks' units come first, with slots of their own count
+                const int slots_s = p.sink_split == 2 ? 1 : p.sink_split, slots_q = nsp == 2 ? 1 : nsp;
+                slot_e = (size_t)part_units * slots_s - (size_t)part_units * slots_q;
+            }
+        }
         int* n_written = SPLIT ? p.split_cnt + p.n_split_units + unit_e : nullptr;
         if (SPLIT && nsp > 1) {
             ok = named_bar_and(3, 128, ok);   // the four warps go on together
@@ -823,8 +887,8 @@ __global__ void __launch_bounds__(384, 1)
             // its own, and a + b = b + a); one per share for more, all stored and added in
             // share order, so that dK / dV do not depend on which CTA finishes last
             const int nslot = nsp == 2 ? 1 : nsp;
-            const int my_slot = (!SPLIT || nsp == 2) ? 0 : (int)(ctaid_x() % (uint32_t)nsp);
-            float4* part = SPLIT ? p.dkv_part + (size_t)unit_e * (size_t)nslot * kPart4 + r : nullptr;
+            const int my_slot = (!SPLIT || nsp == 2) ? 0 : cta_e % nsp;
+            float4* part = SPLIT ? p.dkv_part + (slot_e + (size_t)unit_e * (size_t)nslot) * kPart4 + r : nullptr;
 #pragma unroll 1
             for (int c0 = 0; c0 < C::kDO; c0 += 32) {
                 const int col = fh * C::kDO + c0;   // feature of the tensors in memory

@@ -134,15 +134,17 @@ constexpr CUtensorMapDataType tma_type()
 // {box_inner, box_rows, 1} with box_inner * elt = 128 bytes (the 128-byte
 // swizzle span); elements past `inner` or `rows` read as zero.
 fa_status_t make_map_box(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t outer,
-                         uint32_t elt, uint32_t box_inner, uint32_t box_rows, CUtensorMapDataType dt)
+                         uint32_t elt, uint32_t box_inner, uint32_t box_rows, CUtensorMapDataType dt,
+                         uint64_t outer_rows = 0)
 {
+    // outer_rows: rows between consecutive outer indices in memory (0: `rows`)
     EncodeTiledFn enc = get_encode();
     if (!enc) {
         set_error("cuTensorMapEncodeTiled is unavailable");
         return FA_ERR_CUDA;
     }
     cuuint64_t dims[3] = {inner, rows, outer};
-    cuuint64_t strides[2] = {inner * elt, inner * rows * elt};
+    cuuint64_t strides[2] = {inner * elt, inner * (outer_rows ? outer_rows : rows) * elt};
     cuuint32_t box[3] = {box_inner, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = enc(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
@@ -160,6 +162,13 @@ fa_status_t make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t 
                      uint32_t box_rows, CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)
 {
     return make_map_box(m, base, inner, rows, outer, 2, 64, box_rows, dt);
+}
+
+// The same over the first `rows` of every outer index's `outer_rows` rows (the others read as zero)
+fa_status_t make_map_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t outer_rows,
+                          uint64_t outer, uint32_t box_rows, CUtensorMapDataType dt)
+{
+    return make_map_box(m, base, inner, rows, outer, 2, 64, box_rows, dt, outer_rows);
 }
 
 // 4-D map over a paged KV pool [pages][page_size][Hkv][d] (bf16), box {64, 1, 64, 1}
@@ -329,22 +338,20 @@ struct FwdSplit {
     int shares, full;
 };
 
-FwdSplit fwd_split_plan(const FwdGeom& g, int B, int Hkv, int Nq, int Nk, int d, int causal, int sms)
+// pair_blocks(pr): key blocks of the units of query tile pair pr; kv_bytes: K and V that the
+// launch reads.
+template <typename F>
+FwdSplit fwd_split_search(const FwdGeom& g, int d, int sms, double kv_bytes, F pair_blocks)
 {
     const long long n_units = (long long)g.n_pairs * g.n_bh;
     if (n_units > 8LL * sms || n_units < 1)
         return {1, (int)n_units};
     const int kt = kernel_d(d) == 256 ? 1 : 2;
     // the plan depends on the sizes only through the units' key-block counts
-    const double kv_bytes = 4.0 * B * Hkv * (double)Nk * d;   // K and V, 16-bit
     const bool kv_beyond_l2 = kv_bytes > 64.0 * (1 << 20);
     std::vector<long long> key{g.n_bh, kt, d, sms, kv_beyond_l2};
-    for (int pr = 0; pr < g.n_pairs; ++pr) {
-        int n = 0;
-        for (int t = 0; t < kt; ++t)
-            n = std::max(n, host_blocks_for_tile(pr * 128 * kt + 128 * t, g.rows, Nq, Nk, causal));
-        key.push_back(n);
-    }
+    for (int pr = 0; pr < g.n_pairs; ++pr)
+        key.push_back(pair_blocks(pr));
     static std::mutex mu;
     static std::map<std::vector<long long>, FwdSplit> cache;
     {
@@ -432,6 +439,17 @@ FwdSplit fwd_split_plan(const FwdGeom& g, int B, int Hkv, int Nq, int Nk, int d,
     return best;
 }
 
+FwdSplit fwd_split_plan(const FwdGeom& g, int B, int Hkv, int Nq, int Nk, int d, int causal, int sms)
+{
+    const int kt = kernel_d(d) == 256 ? 1 : 2;
+    return fwd_split_search(g, d, sms, 4.0 * B * Hkv * (double)Nk * d, [&](int pr) {   // K and V, 16-bit
+        int n = 0;
+        for (int t = 0; t < kt; ++t)
+            n = std::max(n, host_blocks_for_tile(pr * 128 * kt + 128 * t, g.rows, Nq, Nk, causal));
+        return n;
+    });
+}
+
 // Test hook state: a slot every tiled forward launch is pinned to (-1: rotate).
 std::atomic<int> g_pinned_slot{-1};
 
@@ -457,10 +475,10 @@ fa_status_t fwd_tile_counter(unsigned** ctr, unsigned* tag)
 
 // The tiled forward's launch: with a key split (p.kv_split > 1) the shares' fp32 partials
 // go to stream-ordered scratch and fwd_combine_kernel merges them into o / lse.
-template <typename T, typename Kern>
+template <typename T, bool WIN = false, typename Kern>
 fa_status_t launch_fwd_tiles(Kern kern, int threads, int smem, const CUtensorMap& mq, const CUtensorMap& mk,
                              const CUtensorMap& mv, fa::FwdParams& p, cudaStream_t stream,
-                             bool after_kernel = false)
+                             bool after_kernel = false, const fa::FwdExtra<WIN>& ex = fa::FwdExtra<WIN>{})
 {
     void* ws = nullptr;
     if (p.kv_split > 1) {
@@ -477,9 +495,9 @@ fa_status_t launch_fwd_tiles(Kern kern, int threads, int smem, const CUtensorMap
     if (after_kernel && p.kv_split <= 1) {
         // straight after a kernel of the same call (the e4m3 V transpose)
         st = launch_dependent("fwd_kernel launch", kern, dim3(fwd_grid(p)), dim3(threads), (size_t)smem, stream,
-                              mq, mk, mv, p);
+                              mq, mk, mv, ex, p);
     } else {
-        kern<<<fwd_grid(p), threads, smem, stream>>>(mq, mk, mv, p);
+        kern<<<fwd_grid(p), threads, smem, stream>>>(mq, mk, mv, ex, p);
         st = check_launch("fwd_kernel launch");
     }
     if (p.kv_split > 1) {
@@ -493,6 +511,32 @@ fa_status_t launch_fwd_tiles(Kern kern, int threads, int smem, const CUtensorMap
             st = cuda_fail(e, "cudaFreeAsync");
     }
     return st;
+}
+
+// The parameters that every tiled forward shares (no window).
+fa::FwdParams fwd_params(const FwdGeom& g, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                         float scale_log2, const FwdSplit& sp)
+{
+    fa::FwdParams p = {};
+    p.o = o;
+    p.lse = lse;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.Nq = Nq;
+    p.Nk = Nk;
+    p.G = Hq / Hkv;
+    p.group_rows = g.group_rows;
+    p.n_bh = g.n_bh;
+    p.rows = g.rows;
+    p.n_pairs = g.n_pairs;
+    p.d_io = d;
+    p.scale_log2 = scale_log2;
+    p.o_scale = 1.f;
+    p.kv_split = sp.shares;
+    p.full_tiles = sp.full;
+    p.pair_rows = kernel_d(d) == 256 ? 128 : 256;
+    return p;
 }
 
 template <int D, bool CAUSAL, typename T>
@@ -511,27 +555,7 @@ fa_status_t launch_fwd(const void* q, const void* k, const void* v, void* o, flo
     const int kv_split = sp.shares;
     auto kern = kv_split > 1 ? fa::fwd_kernel<D, CAUSAL, T, false, true> : fa::fwd_kernel<D, CAUSAL, T, false, false>;
     if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
-    fa::FwdParams p;
-    p.o = o;
-    p.lse = lse;
-    p.B = B;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.Nq = Nq;
-    p.Nk = Nk;
-    p.G = Hq / Hkv;
-    p.group_rows = g.group_rows;
-    p.n_bh = g.n_bh;
-    p.rows = g.rows;
-    p.n_pairs = g.n_pairs;
-    p.d_io = d;
-    p.scale_log2 = scale * kLog2e;
-    p.o_scale = 1.f;
-    p.kv_split = kv_split;
-    p.full_tiles = sp.full;
-    p.pair_rows = 128 * C::kTiles;
-    p.part_o = nullptr;
-    p.part_lse = nullptr;
+    fa::FwdParams p = fwd_params(g, o, lse, B, Hq, Hkv, Nq, Nk, d, scale * kLog2e, sp);
     if ((st = fwd_tile_counter(&p.tile_ctr, &p.tile_tag)) != FA_OK)
         return st;
     return launch_fwd_tiles<T>(kern, C::kThreads, C::kSmemBytes, mq, mk, mv, p, stream);
@@ -570,27 +594,8 @@ fa_status_t launch_fwd_fp8(const void* q, const void* k, const void* v, void* vt
     auto kern = kv_split > 1 ? fa::fwd_kernel<kF8D, CAUSAL, __nv_bfloat16, true, true>
                              : fa::fwd_kernel<kF8D, CAUSAL, __nv_bfloat16, true, false>;
     if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
-    fa::FwdParams p;
-    p.o = o;
-    p.lse = lse;
-    p.B = B;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.Nq = Nq;
-    p.Nk = Nk;
-    p.G = Hq / Hkv;
-    p.group_rows = g.group_rows;
-    p.n_bh = g.n_bh;
-    p.rows = g.rows;
-    p.n_pairs = g.n_pairs;
-    p.d_io = kF8D;
-    p.scale_log2 = scale_log2;
+    fa::FwdParams p = fwd_params(g, o, lse, B, Hq, Hkv, Nq, Nk, kF8D, scale_log2, sp);
     p.o_scale = o_scale;
-    p.kv_split = kv_split;
-    p.full_tiles = sp.full;
-    p.pair_rows = 256;
-    p.part_o = nullptr;
-    p.part_lse = nullptr;
     if ((st = fwd_tile_counter(&p.tile_ctr, &p.tile_tag)) != FA_OK)
         return st;
     return launch_fwd_tiles<__nv_bfloat16>(kern, C::kThreads, C::kSmemBytes, mq, mk, mv, p, stream, true);
@@ -615,6 +620,82 @@ fa_status_t fwd_tiled(int dtype, const void* q, const void* k, const void* v, vo
 {
     return dtype == FA_DTYPE_FP16 ? fwd_tiled_t<__half>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, s)
                                   : fwd_tiled_t<__nv_bfloat16>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, s);
+}
+
+// ---------------------------------------------------------------------------
+// forward with a sliding window and sinks (tiled kernel)
+// ---------------------------------------------------------------------------
+struct Window {
+    int window, sinks;
+};
+
+// The window and the sinks, each cut to the longest history (which sees the same keys).
+fa_status_t check_window(int window, int sinks, int Nk, Window* w)
+{
+    if (window < 1) {
+        set_error("window=%d must be >= 1", window);
+        return FA_ERR_INVALID_ARGUMENT;
+    }
+    if (sinks < 0) {
+        set_error("sinks=%d must be >= 0", sinks);
+        return FA_ERR_INVALID_ARGUMENT;
+    }
+    w->window = std::min(window, Nk);
+    w->sinks = std::min(sinks, Nk);
+    return FA_OK;
+}
+
+template <int D, typename T>
+fa_status_t launch_fwd_win(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
+                           int Nq, int Nk, int d, float scale, const Window& w, cudaStream_t stream)
+{
+    using C = fa::FwdCfg<D>;
+    CUtensorMap mq, mk, mv;
+    fa::FwdExtra<true> ex;
+    fa_status_t st;
+    const FwdGeom g = fwd_geom(B, Hq, Hkv, Nq, d);
+    const uint64_t kvh = (uint64_t)B * Hkv;
+    const int full = w.sinks / 128, rem = (w.sinks % 128 + 7) / 8 * 8;
+    if ((st = make_map(&mq, q, d, g.rows, (uint64_t)g.n_bh, 128, tma_type<T>())) != FA_OK) return st;
+    if ((st = make_map(&mk, k, d, Nk, kvh, 128, tma_type<T>())) != FA_OK) return st;
+    if ((st = make_map(&mv, v, d, Nk, kvh, 128, tma_type<T>())) != FA_OK) return st;
+    ex.k_sink = ex.k_win = mk;   // copies where a box has no rows (never loaded)
+    ex.v_sink = ex.v_win = mv;
+    const void* base[2] = {k, v};
+    CUtensorMap* sink_maps[2] = {&ex.k_sink, &ex.v_sink};
+    CUtensorMap* win_maps[2] = {&ex.k_win, &ex.v_win};
+    for (int i = 0; i < 2 && rem > 0; ++i) {
+        // the sinks' keys alone (rows past them read as zero), and the box after them
+        if ((st = make_map_rows(sink_maps[i], base[i], d, w.sinks, Nk, kvh, rem, tma_type<T>())) != FA_OK) return st;
+        if (rem < 128 && (st = make_map(win_maps[i], base[i], d, Nk, kvh, 128 - rem, tma_type<T>())) != FA_OK) return st;
+    }
+    const double kv_keys = std::min<double>(Nk, (double)w.sinks + w.window + Nq);
+    const FwdSplit sp = fwd_split_search(g, d, sm_count(), 4.0 * B * Hkv * kv_keys * d, [&](int pr) {
+        int lo, nb[2];
+        fa::fwd_win_blocks(pr * 128 * C::kTiles, C::kTiles, g.rows, Nq, Nk, w.window, w.sinks, 128 * full + rem, lo, nb);
+        return std::max(nb[0], nb[1]);
+    });
+    auto kern = sp.shares > 1 ? fa::fwd_kernel<D, true, T, false, true, true> : fa::fwd_kernel<D, true, T, false, false, true>;
+    if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
+    fa::FwdParams p = fwd_params(g, o, lse, B, Hq, Hkv, Nq, Nk, d, scale * kLog2e, sp);
+    p.window = w.window;
+    p.sinks = w.sinks;
+    p.sink_full = full;
+    p.sink_rem = rem;
+    if ((st = fwd_tile_counter(&p.tile_ctr, &p.tile_tag)) != FA_OK)
+        return st;
+    return launch_fwd_tiles<T, true>(kern, C::kThreads, C::kSmemBytes, mq, mk, mv, p, stream, false, ex);
+}
+
+template <typename T>
+fa_status_t fwd_win_t(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Nq,
+                      int Nk, int d, float scale, const Window& w, cudaStream_t s)
+{
+    if (kernel_d(d) == 256)
+        return launch_fwd_win<256, T>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, w, s);
+    if (kernel_d(d) == 128)
+        return launch_fwd_win<128, T>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, w, s);
+    return launch_fwd_win<64, T>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, w, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -686,7 +767,7 @@ struct PagedDesc {
 template <typename T>
 fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
                             int Hkv, int Nq, int Nk, int d, float scale, int causal, const DecodePlan& pl, void* ws,
-                            cudaStream_t stream, const PagedDesc* pg)
+                            cudaStream_t stream, const PagedDesc* pg, const Window* win)
 {
     using C = fa::DecCfg;
     CUtensorMap mk, mv;
@@ -700,6 +781,9 @@ fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o
     }
     auto kern = d < 128 ? (pg ? fa::decode_split_kernel<true, T, true> : fa::decode_split_kernel<false, T, true>)
                         : (pg ? fa::decode_split_kernel<true, T, false> : fa::decode_split_kernel<false, T, false>);
+    if (win)
+        kern = d < 128 ? (pg ? fa::decode_split_kernel<true, T, true, true> : fa::decode_split_kernel<false, T, true, true>)
+                       : (pg ? fa::decode_split_kernel<true, T, false, true> : fa::decode_split_kernel<false, T, false, true>);
     if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
     fa::DecodeParams p;
     p.q = q;
@@ -725,6 +809,8 @@ fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o
     p.seq_lens = pg ? pg->seq_lens : nullptr;
     p.page_size = pg ? pg->page_size : 0;
     p.max_pages = pg ? pg->max_pages : 0;
+    p.window = win ? win->window : 0;
+    p.sinks = win ? win->sinks : 0;
     const long long grid = (long long)B * Hkv * pl.splits;
     kern<<<(unsigned)grid, C::kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
     if ((st = check_launch("decode_split_kernel launch")) != FA_OK) return st;
@@ -739,11 +825,26 @@ fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o
 
 fa_status_t launch_decode(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
                           int Nq, int Nk, int d, float scale, int causal, const DecodePlan& pl, void* ws,
-                          cudaStream_t stream, const PagedDesc* pg = nullptr, int dtype = FA_DTYPE_BF16)
+                          cudaStream_t stream, const PagedDesc* pg = nullptr, int dtype = FA_DTYPE_BF16,
+                          const Window* win = nullptr)
 {
     if (dtype == FA_DTYPE_FP16)
-        return launch_decode_t<__half>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, stream, pg);
-    return launch_decode_t<__nv_bfloat16>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, stream, pg);
+        return launch_decode_t<__half>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, stream, pg, win);
+    return launch_decode_t<__nv_bfloat16>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, stream, pg,
+                                          win);
+}
+
+// Keys of the longest list of visible tiles that a windowed decode may meet: Nk keys in a dense
+// cache, any length up to Nk in a paged one.
+int win_list_keys(int Nq, int Nk, const Window& w, bool paged)
+{
+    int lo, sink_tiles, base;
+    if (!paged)
+        return fa::DecCfg::kKeys * fa::dec_win_tiles(Nk, Nq, w.window, w.sinks, false, lo, sink_tiles, base);
+    // the window's keys start anywhere in their first tile
+    const int kt = fa::DecCfg::kKeys;
+    const long long tiles = (w.sinks + kt - 1) / kt + ((long long)w.window + Nq - 1 + kt - 2) / kt + 1;
+    return (int)std::min<long long>(tiles, (Nk + kt - 1) / kt) * kt;
 }
 
 // ---------------------------------------------------------------------------
@@ -940,7 +1041,70 @@ BwdPlan bwd_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d)
     return pl;
 }
 
-template <int D, bool CAUSAL, typename T>
+// Windowed backward: CTAs per unit of the key blocks that hold sinks (sink_split) and of the
+// others (q_split).  The sinks' units walk every later query, the others only a window's worth,
+// so with equal shares the sinks' would run on long after the rest.  Each choice costs what the
+// CTAs' steps and fixed parts (as in bwd_q_split) take spread over the SMs, and at least the
+// longest CTA; partials stay within 256 MB.
+struct BwdWinPlan {
+    int sink_blocks, sink_split, q_split, n_units;
+    size_t part_off, cnt_off, total_split;
+};
+
+BwdWinPlan bwd_win_plan(const BwdPlan& base, int B, int Hq, int Hkv, int Nq, int Nk, int d, const Window& w, int sms)
+{
+    const int kd = kernel_d(d), G = Hq / Hkv;
+    const int n_kb = (Nk + 127) / 128;
+    const double per_kb = (double)B * Hkv * (kd == 256 ? 2 : 1);
+    BwdWinPlan pl;
+    pl.sink_blocks = std::min(n_kb, (w.sinks + 127) / 128);
+    pl.n_units = base.n_units;
+    double total = 0, longest[2] = {0, 0};
+    for (int kb = 0; kb < n_kb; ++kb) {
+        int qb0, nqb;
+        fa::bwd_win_q_range(kb, Nq, Nk, w.window, w.sinks, qb0, nqb);
+        const double steps = (double)G * nqb;
+        total += steps * per_kb;
+        double& l = longest[kb < pl.sink_blocks ? 0 : 1];
+        l = std::max(l, steps);
+    }
+    static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+    const double slot_bytes = 2.0 * std::min(kd, 128) * 128 * 4;
+    const double sink_units = pl.sink_blocks * per_kb, other_units = (n_kb - pl.sink_blocks) * per_kb;
+    auto slots = [](int s) { return s == 1 ? 0 : s == 2 ? 1 : s; };
+    auto fixed = [](int s) { return 8.5 + (s > 1 ? 0.8 * (s - 1) : 0.0); };
+    pl.sink_split = pl.q_split = 1;
+    double best = 0;
+    for (int ss : kSplits) {
+        if (ss > 1 && (longest[0] < 16.0 * ss || pl.sink_blocks == 0))
+            break;
+        for (int qs : kSplits) {
+            if (qs > 8 || (qs > 1 && longest[1] < 16.0 * qs))
+                break;
+            if (slot_bytes * (sink_units * slots(ss) + other_units * slots(qs)) > 256.0 * (1 << 20))
+                continue;
+            const double work = total + sink_units * ss * fixed(ss) + other_units * qs * fixed(qs);
+            double cost = work / sms;
+            if (pl.sink_blocks > 0)
+                cost = std::max(cost, longest[0] / ss + fixed(ss));
+            // the others come last, all about alike: the last round counts whole
+            if (other_units > 0)
+                cost = std::max(cost, work / sms + 0.5 * (longest[1] / qs + fixed(qs)));
+            if ((ss == 1 && qs == 1) || cost < 0.97 * best) {
+                best = cost;
+                pl.sink_split = ss;
+                pl.q_split = qs;
+            }
+        }
+    }
+    const size_t n_slots = (size_t)(sink_units * slots(pl.sink_split) + other_units * slots(pl.q_split));
+    pl.part_off = base.total;
+    pl.cnt_off = pl.part_off + align256(n_slots * (size_t)slot_bytes);
+    pl.total_split = n_slots ? pl.cnt_off + align256((size_t)pl.n_units * 2 * 4) : base.total;
+    return pl;
+}
+
+template <int D, bool CAUSAL, typename T, bool WIN = false>
 fa_status_t launch_bwd(const fa::BwdParams& p, const void* q, const void* k, const void* v, const void* dout,
                        cudaStream_t stream)
 {
@@ -956,9 +1120,12 @@ fa_status_t launch_bwd(const fa::BwdParams& p, const void* q, const void* k, con
     if ((st = make_map(&mdo, dout, p.d_io, p.Nq, (uint64_t)p.B * p.Hq, 64, dt)) != FA_OK) return st;
     if ((st = make_map(&mk, k, p.d_io, p.Nk, (uint64_t)p.B * p.Hkv, 128, dt)) != FA_OK) return st;
     if ((st = make_map(&mv, v, p.d_io, p.Nk, (uint64_t)p.B * p.Hkv, 128, dt)) != FA_OK) return st;
-    auto kern = p.q_split > 1 ? fa::bwd_main_kernel<D, CAUSAL, T, true> : fa::bwd_main_kernel<D, CAUSAL, T, false>;
+    auto kern = WIN || p.q_split > 1 ? fa::bwd_main_kernel<D, CAUSAL, T, true, WIN>
+                                     : fa::bwd_main_kernel<D, CAUSAL, T, WIN, WIN>;
     if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
-    const long long grid = (long long)((p.Nk + 127) / 128) * p.B * p.Hkv * C::kFeatSplit * p.q_split;
+    const int n_kb = (p.Nk + 127) / 128, n_sink = WIN ? p.sink_blocks : 0;
+    const long long grid = (long long)p.B * p.Hkv * C::kFeatSplit *
+                           ((long long)n_sink * p.sink_split + (long long)(n_kb - n_sink) * p.q_split);
     if ((st = launch_dependent("bwd_main_kernel launch", kern, dim3((unsigned)grid), dim3(C::kThreads),
                                C::kSmemBytes, stream, mq, mk, mv, mdo, p)) != FA_OK)
         return st;
@@ -978,6 +1145,17 @@ fa_status_t bwd_dispatch(const fa::BwdParams& p, const void* q, const void* k, c
     if (kd == 128)
         return causal ? launch_bwd<128, true, T>(p, q, k, v, dout, s) : launch_bwd<128, false, T>(p, q, k, v, dout, s);
     return causal ? launch_bwd<64, true, T>(p, q, k, v, dout, s) : launch_bwd<64, false, T>(p, q, k, v, dout, s);
+}
+
+template <typename T>
+fa_status_t bwd_win_dispatch(const fa::BwdParams& p, const void* q, const void* k, const void* v, const void* dout,
+                             int kd, cudaStream_t s)
+{
+    if (kd == 256)
+        return launch_bwd<256, true, T, true>(p, q, k, v, dout, s);
+    if (kd == 128)
+        return launch_bwd<128, true, T, true>(p, q, k, v, dout, s);
+    return launch_bwd<64, true, T, true>(p, q, k, v, dout, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -1024,8 +1202,10 @@ const char* fa_status_string(fa_status_t s)
 const char* fa_last_error_message(void) { return t_error.c_str(); }
 
 static fa_status_t fwd_entry(int dtype, const void* q, const void* k, const void* v, void* o, float* lse, int B,
-                             int Hq, int Hkv, int Nq, int Nk, int d, float scale, int causal, void* stream)
+                             int Hq, int Hkv, int Nq, int Nk, int d, float scale, int causal, void* stream,
+                             const int* window = nullptr)
 {
+    // window: {window, sinks} of the windowed forward (causal), or null
     t_error.clear();
     fa_status_t st;
     if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_FP16) {
@@ -1041,17 +1221,25 @@ static fa_status_t fwd_entry(int dtype, const void* q, const void* k, const void
     }
     if ((st = check_shape(B, Hq, Hkv, Nq, Nk, d, scale, causal)) != FA_OK)
         return st;
+    Window win = {};
+    if (window && (st = check_window(window[0], window[1], Nk, &win)) != FA_OK)
+        return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!decode_shape(Hq, Hkv, Nq, d))
+    if (!decode_shape(Hq, Hkv, Nq, d)) {
+        if (window)
+            return dtype == FA_DTYPE_FP16 ? fwd_win_t<__half>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, win, s)
+                                          : fwd_win_t<__nv_bfloat16>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, win, s);
         return fwd_tiled(dtype, q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, s);
-    const DecodePlan pl = decode_plan(B, Hq, Hkv, Nq, Nk, d, 0);
+    }
+    const DecodePlan pl = decode_plan(B, Hq, Hkv, Nq, window ? win_list_keys(Nq, Nk, win, false) : Nk, d, 0);
     void* ws = nullptr;
     if (pl.total() > 0) {
         cudaError_t e = scratch_alloc(&ws, pl.total(), s);
         if (e != cudaSuccess)
             return cuda_fail(e, "scratch allocation (split-KV partials)");
     }
-    st = launch_decode(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, s, nullptr, dtype);
+    st = launch_decode(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, s, nullptr, dtype,
+                       window ? &win : nullptr);
     if (ws) {
         cudaError_t e = cudaFreeAsync(ws, s);
         if (e != cudaSuccess && st == FA_OK)
@@ -1253,7 +1441,7 @@ static fa_status_t paged_entry(int dtype, const void* q, const void* k_cache, co
                                const int* block_table, const int* seq_lens, void* o, float* lse, int B, int Hq,
                                int Hkv, int Nq, int d, int page_size, int num_pages, int max_pages_per_seq,
                                float scale, int causal, int num_splits, void* workspace, size_t workspace_bytes,
-                               void* stream)
+                               void* stream, const int* window = nullptr)
 {
     t_error.clear();
     fa_status_t st;
@@ -1294,7 +1482,11 @@ static fa_status_t paged_entry(int dtype, const void* q, const void* k_cache, co
         return FA_ERR_INVALID_ARGUMENT;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const DecodePlan pl = decode_plan(B, Hq, Hkv, Nq, max_len, d, num_splits);
+    Window win = {};
+    if (window && (st = check_window(window[0], window[1], max_len, &win)) != FA_OK)
+        return st;
+    const int plan_keys = window ? win_list_keys(Nq, max_len, win, true) : max_len;
+    const DecodePlan pl = decode_plan(B, Hq, Hkv, Nq, plan_keys, d, num_splits);
     void* ws = workspace;
     bool owned = false;
     if (pl.total() > 0) {
@@ -1310,7 +1502,7 @@ static fa_status_t paged_entry(int dtype, const void* q, const void* k_cache, co
     }
     PagedDesc pg{block_table, seq_lens, page_size, num_pages, max_pages_per_seq};
     st = launch_decode(q, k_cache, v_cache, o, lse, B, Hq, Hkv, Nq, max_len, d, scale, causal, pl, ws, s, &pg,
-                       dtype);
+                       dtype, window ? &win : nullptr);
     if (owned) {
         cudaError_t e = cudaFreeAsync(ws, s);
         if (e != cudaSuccess && st == FA_OK)
@@ -1368,8 +1560,9 @@ int fa_bwd_query_split(int B, int Hq, int Hkv, int Nq, int Nk, int d, int causal
 static fa_status_t bwd_entry(int dtype, const void* q, const void* k, const void* v, const void* o,
                              const void* dout, const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv,
                              int Nq, int Nk, int d, float scale, int causal, void* workspace,
-                             size_t workspace_bytes, void* stream)
+                             size_t workspace_bytes, void* stream, const int* window = nullptr)
 {
+    // window: {window, sinks} of the windowed backward (causal), or null
     t_error.clear();
     fa_status_t st;
     if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_FP16) {
@@ -1386,23 +1579,40 @@ static fa_status_t bwd_entry(int dtype, const void* q, const void* k, const void
         set_error("workspace is not 256-byte aligned");
         return FA_ERR_INVALID_ARGUMENT;
     }
-    const BwdPlan pl = bwd_plan(B, Hq, Hkv, Nq, Nk, d);
+    Window win = {};
+    if (window && (st = check_window(window[0], window[1], Nk, &win)) != FA_OK)
+        return st;
+    BwdPlan pl = bwd_plan(B, Hq, Hkv, Nq, Nk, d);
     if (workspace && workspace_bytes < pl.total) {
         set_error("workspace has %zu bytes, %zu needed", workspace_bytes, pl.total);
         return FA_ERR_WORKSPACE;
     }
+    int sink_split = 1, sink_blocks = 0;
+    if (window) {
+        const BwdWinPlan wp = bwd_win_plan(pl, B, Hq, Hkv, Nq, Nk, d, win, sm_count());
+        pl.q_split[1] = wp.q_split;
+        pl.part_off = wp.part_off;
+        pl.cnt_off = wp.cnt_off;
+        pl.total_split = wp.total_split;
+        sink_split = wp.sink_split;
+        sink_blocks = wp.sink_blocks;
+    }
     // the query split needs the partials' room too: a smaller workspace runs without it
-    const int q_split = (!workspace || workspace_bytes >= pl.total_split) ? pl.q_split[causal ? 1 : 0] : 1;
+    const bool may_split = !workspace || workspace_bytes >= pl.total_split;
+    const int q_split = may_split ? pl.q_split[causal ? 1 : 0] : 1;
+    if (!may_split)
+        sink_split = 1;
+    const bool split = q_split > 1 || sink_split > 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void* ws = workspace;
     bool owned = false;
     if (!ws) {
-        cudaError_t e = scratch_alloc(&ws, q_split > 1 ? pl.total_split : pl.total, s);
+        cudaError_t e = scratch_alloc(&ws, split ? pl.total_split : pl.total, s);
         if (e != cudaSuccess)
             return cuda_fail(e, "scratch allocation (backward workspace)");
         owned = true;
     }
-    fa::BwdParams p;
+    fa::BwdParams p = {};
     p.q = q;
     p.k = k;
     p.v = v;
@@ -1429,10 +1639,18 @@ static fa_status_t bwd_entry(int dtype, const void* q, const void* k, const void
     p.scale_log2 = scale * kLog2e;
     p.q_split = q_split;
     p.n_split_units = pl.n_units;
-    p.dkv_part = q_split > 1 ? reinterpret_cast<float4*>(w + pl.part_off) : nullptr;
-    p.split_cnt = q_split > 1 ? reinterpret_cast<int*>(w + pl.cnt_off) : nullptr;
-    st = dtype == FA_DTYPE_FP16 ? bwd_dispatch<__half>(p, q, k, v, dout, kernel_d(d), causal, s)
-                                : bwd_dispatch<__nv_bfloat16>(p, q, k, v, dout, kernel_d(d), causal, s);
+    p.dkv_part = split ? reinterpret_cast<float4*>(w + pl.part_off) : nullptr;
+    p.split_cnt = split ? reinterpret_cast<int*>(w + pl.cnt_off) : nullptr;
+    p.window = win.window;
+    p.sinks = win.sinks;
+    p.sink_blocks = sink_blocks;
+    p.sink_split = sink_split;
+    if (window)
+        st = dtype == FA_DTYPE_FP16 ? bwd_win_dispatch<__half>(p, q, k, v, dout, kernel_d(d), s)
+                                    : bwd_win_dispatch<__nv_bfloat16>(p, q, k, v, dout, kernel_d(d), s);
+    else
+        st = dtype == FA_DTYPE_FP16 ? bwd_dispatch<__half>(p, q, k, v, dout, kernel_d(d), causal, s)
+                                    : bwd_dispatch<__nv_bfloat16>(p, q, k, v, dout, kernel_d(d), causal, s);
     if (owned) {
         cudaError_t e = cudaFreeAsync(ws, s);
         if (e != cudaSuccess && st == FA_OK)
@@ -1456,6 +1674,53 @@ fa_status_t fa_bwd_ex(fa_dtype_t dtype, const void* q, const void* k, const void
 {
     return bwd_entry((int)dtype, q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, Nq, Nk, d, scale, causal,
                      workspace, workspace_bytes, stream);
+}
+
+fa_status_t fa_fwd_window(fa_dtype_t dtype, const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                          int Hq, int Hkv, int Nq, int Nk, int d, float scale, int window, int sinks, void* stream)
+{
+    const int w[2] = {window, sinks};
+    return fwd_entry((int)dtype, q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, 1, stream, w);
+}
+
+size_t fa_bwd_window_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int d, int window, int sinks)
+{
+    if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Nk < 1 || Hq % Hkv != 0 || d < 1 || d > 256 || window < 1 || sinks < 0)
+        return 0;
+    const Window w{std::min(window, Nk), std::min(sinks, Nk)};
+    return bwd_win_plan(bwd_plan(B, Hq, Hkv, Nq, Nk, d), B, Hq, Hkv, Nq, Nk, d, w, sm_count()).total_split;
+}
+
+fa_status_t fa_bwd_window(fa_dtype_t dtype, const void* q, const void* k, const void* v, const void* o,
+                          const void* dout, const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv,
+                          int Nq, int Nk, int d, float scale, int window, int sinks, void* workspace,
+                          size_t workspace_bytes, void* stream)
+{
+    const int w[2] = {window, sinks};
+    return bwd_entry((int)dtype, q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, Nq, Nk, d, scale, 1, workspace,
+                     workspace_bytes, stream, w);
+}
+
+size_t fa_fwd_paged_window_workspace_size(int B, int Hq, int Hkv, int Nq, int page_size, int max_pages_per_seq, int d,
+                                          int window, int sinks, int num_splits)
+{
+    if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Hq % Hkv != 0 || d < 1 || num_splits < 0 || page_size < 1 ||
+        max_pages_per_seq < 1 || (long long)page_size * max_pages_per_seq > (1ll << 30) || window < 1 || sinks < 0)
+        return 0;
+    const int max_len = page_size * max_pages_per_seq;
+    const Window w{std::min(window, max_len), std::min(sinks, max_len)};
+    return decode_plan(B, Hq, Hkv, Nq, win_list_keys(Nq, max_len, w, true), d, num_splits).total();
+}
+
+fa_status_t fa_fwd_paged_window(fa_dtype_t dtype, const void* q, const void* k_cache, const void* v_cache,
+                                const int* block_table, const int* seq_lens, void* o, float* lse, int B, int Hq,
+                                int Hkv, int Nq, int d, int page_size, int num_pages, int max_pages_per_seq,
+                                float scale, int window, int sinks, int num_splits, void* workspace,
+                                size_t workspace_bytes, void* stream)
+{
+    const int w[2] = {window, sinks};
+    return paged_entry((int)dtype, q, k_cache, v_cache, block_table, seq_lens, o, lse, B, Hq, Hkv, Nq, d, page_size,
+                       num_pages, max_pages_per_seq, scale, 1, num_splits, workspace, workspace_bytes, stream, w);
 }
 
 fa_status_t fa_check_device_status(void* stream)

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 namespace fa {
@@ -36,6 +37,23 @@ struct FwdParams {
     int pair_rows;      // query rows of a work unit: 256 (128 at d = 256)
     float* part_o;      // [n_bh, kv_split, rows, d_io] fp32: O_s = U_s / l_s of share s
     float* part_lse;    // [n_bh, kv_split, rows] fp32: m_s + log2(l_s), -inf where share s sees no key
+    // sliding window with sinks (fwd_kernel<..., WIN = true>, causal): key j is visible at query
+    // position x (in keys: i + Nk - Nq) iff j <= x and (j > x - window or j < sinks)
+    int window;         // 1 .. Nk
+    int sinks;          // 0 .. Nk
+    int sink_full;      // whole 128-key blocks of sinks: sinks / 128
+    int sink_rem;       // rows of the block after them that hold the other sinks, a multiple of 8
+                        // (0: no such block; 128: it holds no window keys)
+};
+
+// Extra TMA maps of a windowed forward: the block that holds both sinks and window keys is two
+// boxes, sink_rem rows of the first `sinks` keys (zero fill past them) and 128 - sink_rem rows
+// from the window's first key.
+template <bool WIN>
+struct FwdExtra {};
+template <>
+struct FwdExtra<true> {
+    CUtensorMap k_sink, v_sink, k_win, v_win;
 };
 
 struct DecodeParams {
@@ -62,6 +80,10 @@ struct DecodeParams {
     const int* seq_lens;     // [B]
     int page_size;
     int max_pages;
+    // sliding window with sinks (decode_split_kernel<..., WIN = true>), as in FwdParams;
+    // `chunk` then counts keys of the visible tiles' list
+    int window;
+    int sinks;
 };
 
 struct BwdParams {
@@ -90,7 +112,14 @@ struct BwdParams {
     int q_split;
     int n_split_units;          // units of the launch (q_split > 1)
     float4* dkv_part;           // [n_split_units][q_split == 2 ? 1 : q_split][2 * dK/dV features / 4][128]
-    int* split_cnt;             // [2][n_split_units]: tickets taken, partials written
+    int* split_cnt;             // [2][n_split_units]: tickets taken, partials written; null without a split
+    // sliding window with sinks (bwd_main_kernel<..., WIN = true>), as in FwdParams.  The key
+    // blocks below sink_blocks hold sinks, which every later query sees: their units are shared
+    // by sink_split CTAs, the others by q_split
+    int window;
+    int sinks;
+    int sink_blocks;
+    int sink_split;
 };
 
 }  // namespace fa

@@ -117,6 +117,47 @@ __device__ __forceinline__ int fwd_blocks_for_tile(int qt, int rows, int Nq, int
     return min(nkb, last_key / 128 + 1);
 }
 
+// Positions of the query rows [qt, qt + 128) of a tile head: smallest and largest (row r at
+// position r % Nq).  Only for qt < rows.
+__host__ __device__ __forceinline__ void fwd_positions(int qt, int rows, int Nq, int& lo, int& hi)
+{
+    const int last_row = qt + 127 < rows ? qt + 127 : rows - 1;
+    const bool one = qt / Nq == last_row / Nq;
+    lo = one ? qt % Nq : 0;
+    hi = one ? last_row % Nq : Nq - 1;
+}
+
+// Key blocks of a work tile (query tiles at rows q0 and, with kTiles = 2, q0 + 128) under a
+// sliding window with sinks.  The tile's keys form one list: the sinks padded to
+// S8 = 128 sink_full + sink_rem places, then the window's keys from `lo` on, the first key of
+// the tile's smallest position (never below the sinks, so no key is in the list twice).  Block j
+// is places 128 j .. 128 j + 127.  nb[t] is the number of blocks up to the last key that query
+// tile t sees.
+__host__ __device__ __forceinline__ void fwd_win_blocks(int q0, int tiles, int rows, int Nq, int Nk, int window,
+                                                        int sinks, int sink_places, int& lo, int (&nb)[2])
+{
+    const int delta = Nk - Nq;
+    int pmin = INT_MAX, hi[2] = {0, 0};
+    for (int t = 0; t < tiles; ++t) {
+        if (q0 + 128 * t >= rows)
+            continue;
+        int a, b;
+        fwd_positions(q0 + 128 * t, rows, Nq, a, b);
+        pmin = pmin < a ? pmin : a;
+        hi[t] = b + delta + 1;   // keys below hi (at most Nk)
+    }
+    const int first = pmin == INT_MAX ? sinks : pmin + delta - window + 1;
+    lo = first > sinks ? first : sinks;
+    for (int t = 0; t < 2; ++t) {
+        if (hi[t] <= 0)
+            nb[t] = 0;
+        else if (hi[t] > lo)
+            nb[t] = (sink_places + hi[t] - lo + 127) / 128;
+        else   // only sinks (lo = sinks)
+            nb[t] = (hi[t] + 127) / 128;
+    }
+}
+
 // Tile counters of the forward launches, four words per slot: tiles claimed
 // beyond each block's first, blocks that have stopped claiming, the owner tag
 // of the launch using the slot (0 = free), and padding.  Each launch takes the
@@ -144,6 +185,7 @@ struct FwdTile {
     int kb0;       // first key block of the share (0 without a key split)
     int share;     // key share (0 without a key split)
     int nshares;   // key shares of the tile's unit (1: the whole unit, written straight to o / lse)
+    int wlo;       // sliding window: first window key of the tile (fwd_win_blocks)
 };
 
 // The launch has at most one block per SM.  Block c starts with tile c; each
@@ -151,7 +193,7 @@ struct FwdTile {
 // hardware block scheduler the blocks take the heavy causal tiles first and
 // whichever block is free takes the next.  With a key split (SPLIT) tile i is
 // share (i / (B*Hq)) % kv_split of its pair's key blocks.
-template <int kTiles, bool CAUSAL, bool SPLIT = false>
+template <int kTiles, bool CAUSAL, bool SPLIT = false, bool WIN = false>
 __device__ __forceinline__ void fwd_tile(const FwdParams& p, int i, FwdTile& w)
 {
     const int n_bh = p.n_bh;
@@ -175,8 +217,15 @@ __device__ __forceinline__ void fwd_tile(const FwdParams& p, int i, FwdTile& w)
         w.kvh = b * p.Hkv + h / p.G;
     }
     w.q0 = pair * 128 * kTiles;
-    w.nb0 = fwd_blocks_for_tile(w.q0, p.rows, p.Nq, p.Nk, CAUSAL);
-    w.nb1 = (kTiles == 2) ? fwd_blocks_for_tile(w.q0 + 128, p.rows, p.Nq, p.Nk, CAUSAL) : 0;
+    if constexpr (WIN) {
+        int nb[2];
+        fwd_win_blocks(w.q0, kTiles, p.rows, p.Nq, p.Nk, p.window, p.sinks, 128 * p.sink_full + p.sink_rem, w.wlo, nb);
+        w.nb0 = nb[0];
+        w.nb1 = nb[1];
+    } else {
+        w.nb0 = fwd_blocks_for_tile(w.q0, p.rows, p.Nq, p.Nk, CAUSAL);
+        w.nb1 = (kTiles == 2) ? fwd_blocks_for_tile(w.q0 + 128, p.rows, p.Nq, p.Nk, CAUSAL) : 0;
+    }
     w.kb0 = 0;
     if (SPLIT && ns > 1) {
         // blocks [lo, hi) of the pair's n; a tile sees the part of them below its own count
@@ -205,12 +254,14 @@ __device__ __forceinline__ int fwd_take_tile(uint64_t* bar_tfull, uint64_t* bar_
 }
 
 // SPLIT: key split (kv_split shares per pair, partial results to part_o / part_lse);
-// without it the kernel carries none of the split's code
-template <int D, bool CAUSAL, typename T = __nv_bfloat16, bool F8 = false, bool SPLIT = false>
+// without it the kernel carries none of the split's code.  WIN: sliding window with
+// sinks; only the tile's list of key blocks, their loads and their masks differ.
+template <int D, bool CAUSAL, typename T = __nv_bfloat16, bool F8 = false, bool SPLIT = false, bool WIN = false>
 __global__ void __launch_bounds__(384, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-               const __grid_constant__ CUtensorMap tmV, FwdParams p)
+               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdExtra<WIN> ex, FwdParams p)
 {
+    static_assert(!WIN || (CAUSAL && !F8), "the window is causal, for 16-bit inputs");
     using C = FwdCfg<D, F8>;
     griddep_launch_dependents();   // the merge of a key split may be scheduled
     extern __shared__ uint8_t smem_raw[];
@@ -293,6 +344,30 @@ __global__ void __launch_bounds__(384, 1)
             int kn = 0, vn = 0;     // one-tile blocks: K loads (slot 0) and V loads (slot 1) so far
             bool ok = true;
             int tile = (int)blockIdx.x;
+            // key block j of the tile's share (K for kv = 0, V for 1) into a ring slot
+            auto load_block = [&](uint8_t* dst, uint64_t* bar, int j, int kv) {
+                const CUtensorMap* tm = kv ? &tmV : &tmK;
+                int key = (w.kb0 + j) * 128;
+                if constexpr (WIN) {
+                    const int jb = w.kb0 + j, rem = p.sink_rem;
+                    if (jb >= p.sink_full) {
+                        key = w.wlo + (jb - p.sink_full) * 128 - rem;
+                        if (jb == p.sink_full && rem > 0) {
+                            // sinks and window keys: two boxes of whole 8-row swizzle atoms
+                            for (int pn = 0; pn < C::kPanels; ++pn) {
+                                uint8_t* d = dst + pn * C::kPanelBytes;
+                                tma_load_3d(d, kv ? &ex.v_sink : &ex.k_sink, bar, pn * C::kPanelElems, jb * 128, w.kvh);
+                                if (rem < 128)
+                                    tma_load_3d(d + rem * 128, kv ? &ex.v_win : &ex.k_win, bar, pn * C::kPanelElems,
+                                                w.wlo, w.kvh);
+                            }
+                            return;
+                        }
+                    }
+                }
+                for (int pn = 0; pn < C::kPanels; ++pn)
+                    tma_load_3d(dst + pn * C::kPanelBytes, tm, bar, pn * C::kPanelElems, key, w.kvh);
+            };
             // take the counter slot for this launch, or find it held by another one
             const unsigned owner = atomicCAS(p.tile_ctr + 2, 0u, p.tile_tag);
             const bool own_slot = (owner == 0u || owner == p.tile_tag);
@@ -306,7 +381,7 @@ __global__ void __launch_bounds__(384, 1)
                 mbar_arrive(&bar_tfull[u & 1]);
                 if (tile >= n_tiles)
                     break;
-                fwd_tile<C::kTiles, CAUSAL, SPLIT>(p, tile, w);
+                fwd_tile<C::kTiles, CAUSAL, SPLIT, WIN>(p, tile, w);
                 for (int t = 0; t < 2 && ok; ++t) {
                     if ((t ? w.nb1 : w.nb0) == 0)
                         continue;
@@ -334,9 +409,7 @@ __global__ void __launch_bounds__(384, 1)
                             return false;
                         uint8_t* dst = sKV + kv * C::kTileBytes;
                         mbar_arrive_expect_tx(&bar_full[kv], C::kTileBytes);
-                        for (int pn = 0; pn < C::kPanels; ++pn)
-                            tma_load_3d(dst + pn * C::kPanelBytes, kv ? &tmV : &tmK, &bar_full[kv],
-                                        pn * C::kPanelElems, (w.kb0 + j) * 128, w.kvh);
+                        load_block(dst, &bar_full[kv], j, kv);
                         ++cnt;
                         return true;
                     };
@@ -361,9 +434,7 @@ __global__ void __launch_bounds__(384, 1)
                         if (F8 && kv)   // V^T: d rows of keys j*128 .. j*128+127
                             tma_load_3d(dst, &tmV, &bar_full[slot], (w.kb0 + j) * 128, 0, w.kvh);
                         else
-                            for (int pn = 0; pn < C::kPanels; ++pn)
-                                tma_load_3d(dst + pn * C::kPanelBytes, kv ? &tmV : &tmK, &bar_full[slot],
-                                            pn * C::kPanelElems, (w.kb0 + j) * 128, w.kvh);
+                            load_block(dst, &bar_full[slot], j, kv);
                         ++kvi;
                     }
                 }
@@ -471,7 +542,7 @@ __global__ void __launch_bounds__(384, 1)
                 const int tile = fwd_take_tile(bar_tfull, bar_tfree, tile_ring, u, lane, abort_flag, ok);
                 if (!ok || tile >= n_tiles)
                     break;
-                fwd_tile<C::kTiles, CAUSAL, SPLIT>(p, tile, w);
+                fwd_tile<C::kTiles, CAUSAL, SPLIT, WIN>(p, tile, w);
                 for (int t = 0; t < 2 && ok; ++t) {
                     if ((t ? w.nb1 : w.nb0) == 0)
                         continue;
@@ -617,7 +688,7 @@ __global__ void __launch_bounds__(384, 1)
             const int tile = fwd_take_tile(bar_tfull, bar_tfree, tile_ring, u, lane, abort_flag, ok);
             if (!ok || tile >= n_tiles)
                 break;
-            fwd_tile<C::kTiles, CAUSAL, SPLIT>(p, tile, w);
+            fwd_tile<C::kTiles, CAUSAL, SPLIT, WIN>(p, tile, w);
             const int qi = w.q0 + 128 * t + r;   // row of the tile head
             const int nb = t ? w.nb1 : w.nb0;
             const int qlim = (p.group_rows ? qi % p.Nq : qi) + delta;   // last key its query position sees
@@ -641,8 +712,28 @@ __global__ void __launch_bounds__(384, 1)
                     s[c] = __uint_as_float(sr[c]);
 
                 const int kb = (w.kb0 + j) * 128;
-                const bool need_mask = (kb + 128 > p.Nk) || (CAUSAL && kb + 127 > qlim);
-                if (need_mask) {
+                bool need_mask;
+                if constexpr (WIN) {
+                    // columns below `cut` are sinks, visible up to column shi; the others are
+                    // window keys kw + c, visible from column wlo to whi
+                    const int jb = w.kb0 + j;
+                    const int cut = jb < p.sink_full ? 128 : jb == p.sink_full ? p.sink_rem : 0;
+                    const int shi = min(p.sinks - 1, qlim) - kb;
+                    const int kw = w.wlo + (jb - p.sink_full) * 128 - p.sink_rem;
+                    int wlo = max(p.sinks, qlim - p.window + 1) - kw, whi = qlim - kw;
+                    if (whi < wlo)
+                        wlo = whi = 128;
+                    need_mask = (cut > 0 && shi < cut - 1) || (cut < 128 && (wlo > cut || whi < 127));
+                    if (need_mask) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c)
+                            if (c < cut ? c > shi : (unsigned)(c - wlo) > (unsigned)(whi - wlo))
+                                s[c] = -INFINITY;
+                    }
+                } else {
+                    need_mask = (kb + 128 > p.Nk) || (CAUSAL && kb + 127 > qlim);
+                }
+                if (!WIN && need_mask) {
                     const int lim = CAUSAL ? min(p.Nk - 1, qlim) : p.Nk - 1;
 #pragma unroll
                     for (int c = 0; c < 128; ++c)

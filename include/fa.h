@@ -317,6 +317,53 @@ fa_status_t fa_bwd_ex(fa_dtype_t dtype, const void* q, const void* k, const void
                       void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Attention with a sliding window and sinks: key j is visible to the query at
+ * position x (query row i: x = i + (Nk - Nq)) iff
+ *     j <= x  and  (j > x - window  or  j < sinks),
+ * that is, each query sees the `window` newest keys up to its own and the first
+ * `sinks` keys of the sequence.  Always causal (bottom-right aligned, as above);
+ * window >= 1, sinks >= 0, either may exceed Nk (window >= Nk is fa_fwd with
+ * causal = 1).  Only the key blocks that hold a visible key are read.  Keys that
+ * no query row of the call sees may hold anything, NaN included.
+ * Arguments, kernels and scratch otherwise as fa_fwd_ex (causal = 1): decode
+ * shapes run the split-KV kernels, others the tiled one with its group rows and
+ * key split.  The pages describe neither; they are the usual way to bound the
+ * cost of §04's recurrence for long histories.
+ */
+fa_status_t fa_fwd_window(fa_dtype_t dtype, const void* q, const void* k, const void* v, void* o, float* lse,
+                          int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, int window, int sinks,
+                          void* stream);
+
+/*
+ * Backward of fa_fwd_window: arguments as fa_bwd_ex with the forward's window
+ * and sinks.  A key block is only visited by the queries that see it.  The
+ * blocks that hold sinks, which every later query sees, are shared between
+ * several CTAs (fp32 partials in the workspace, added in a fixed order).
+ * dk and dv of keys that no query sees are 0.  workspace:
+ * fa_bwd_window_workspace_size() bytes, 256-byte aligned, or NULL; one of at
+ * least the size without the partials runs unshared.
+ */
+size_t fa_bwd_window_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int d, int window, int sinks);
+fa_status_t fa_bwd_window(fa_dtype_t dtype, const void* q, const void* k, const void* v, const void* o,
+                          const void* dout, const float* lse, void* dq, void* dk, void* dv, int B, int Hq,
+                          int Hkv, int Nq, int Nk, int d, float scale, int window, int sinks, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * fa_fwd_window over a paged KV cache: arguments as fa_fwd_paged_ex (causal),
+ * with the window against each sequence's own length.  Pages that hold no
+ * visible key are not read (their table entries may be anything), and what a
+ * sequence's last page holds past its length does not matter.
+ */
+size_t fa_fwd_paged_window_workspace_size(int B, int Hq, int Hkv, int Nq, int page_size, int max_pages_per_seq,
+                                          int d, int window, int sinks, int num_splits);
+fa_status_t fa_fwd_paged_window(fa_dtype_t dtype, const void* q, const void* k_cache, const void* v_cache,
+                                const int* block_table, const int* seq_lens, void* o, float* lse, int B, int Hq,
+                                int Hkv, int Nq, int d, int page_size, int num_pages, int max_pages_per_seq,
+                                float scale, int window, int sinks, int num_splits, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
  * Reads and clears the device status word of the current device.  Synchronises
  * `stream` (the only call that does).  Returns FA_OK; FA_ERR_SLOT_CONFLICT if a
  * tiled forward found its tile-counter slot held by another launch since the

@@ -1,0 +1,64 @@
+"""What the windowed calls refuse, before anything touches CUDA."""
+import ctypes
+
+import pytest
+import torch
+
+import exact_attention_114_b200 as fa
+
+FAKE = ctypes.c_void_p(0x10000)
+
+
+def fwd(dtype=0, q=FAKE, lse=None, B=1, Hq=2, Hkv=1, Nq=300, Nk=300, d=64, scale=0.1, window=10, sinks=0):
+    return fa.lib().fa_fwd_window(dtype, q, FAKE, FAKE, FAKE, lse, B, Hq, Hkv, Nq, Nk, d, scale, window, sinks, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=2), fa.FA_ERR_INVALID_ARGUMENT), (dict(q=None), fa.FA_ERR_INVALID_ARGUMENT),
+    (dict(q=ctypes.c_void_p(0x10008)), fa.FA_ERR_INVALID_ARGUMENT),
+    (dict(lse=ctypes.c_void_p(0x10002)), fa.FA_ERR_INVALID_ARGUMENT),
+    (dict(window=0), fa.FA_ERR_INVALID_ARGUMENT), (dict(window=-1), fa.FA_ERR_INVALID_ARGUMENT),
+    (dict(sinks=-1), fa.FA_ERR_INVALID_ARGUMENT), (dict(Nq=0), fa.FA_ERR_INVALID_ARGUMENT),
+    (dict(Hq=3, Hkv=2), fa.FA_ERR_INVALID_ARGUMENT), (dict(scale=-1.0), fa.FA_ERR_INVALID_ARGUMENT),
+    (dict(d=80), fa.FA_ERR_UNSUPPORTED), (dict(d=288), fa.FA_ERR_UNSUPPORTED),
+])
+def test_forward_refuses(kw, status):
+    assert fwd(**kw) == status and fa.last_error_message()
+
+
+def test_backward_refuses():
+    def bwd(ws=None, n=0, window=10, sinks=1, d=64, **over):
+        return fa.lib().fa_bwd_window(0, *[FAKE] * 9, 1, 2, 1, 300, 300, d, 0.1, window, sinks, ws, n, None)
+
+    assert bwd(window=0) == fa.FA_ERR_INVALID_ARGUMENT
+    assert bwd(sinks=-5) == fa.FA_ERR_INVALID_ARGUMENT
+    assert bwd(d=40) == fa.FA_ERR_UNSUPPORTED
+    assert bwd(ws=ctypes.c_void_p(0x100010), n=1 << 30) == fa.FA_ERR_INVALID_ARGUMENT
+    assert bwd(ws=ctypes.c_void_p(0x100000), n=1024) == fa.FA_ERR_WORKSPACE
+    assert fa.fa_bwd_window_workspace_size(1, 2, 1, 300, 300, 64, 0) == 0
+    assert fa.fa_bwd_window_workspace_size(1, 2, 1, 300, 300, 64, 10, -1) == 0
+    assert fa.fa_bwd_window_workspace_size(1, 2, 1, 300, 300, 64, 10, 4) >= 2 * 2 * 320 * 4 + 2 * 320 * 64 * 4
+
+
+def test_paged_refuses():
+    def call(window=10, sinks=0, page=64, Nq=1, d=128, table=FAKE, ws=None, n=0, splits=0):
+        return fa.lib().fa_fwd_paged_window(0, FAKE, FAKE, FAKE, table, FAKE, FAKE, None, 2, 8, 2, Nq, d, page, 100,
+                                            20, 0.1, window, sinks, splits, ws, n, None)
+
+    assert call(window=0) == fa.FA_ERR_INVALID_ARGUMENT
+    assert call(sinks=-1) == fa.FA_ERR_INVALID_ARGUMENT
+    assert call(page=32) == fa.FA_ERR_INVALID_ARGUMENT
+    assert call(table=None) == fa.FA_ERR_INVALID_ARGUMENT
+    assert call(Nq=8) == fa.FA_ERR_UNSUPPORTED
+    assert call(d=256) == fa.FA_ERR_UNSUPPORTED
+    need = fa.fa_fwd_paged_window_workspace_size(2, 8, 2, 1, 64, 20, 128, 500, 4, 3)
+    assert need > 0 and call(window=500, sinks=4, splits=3, ws=ctypes.c_void_p(0x100000), n=need - 16) == fa.FA_ERR_WORKSPACE
+    assert fa.fa_fwd_paged_window_workspace_size(2, 8, 2, 1, 64, 20, 128, 0, 4, 3) == 0
+
+
+def test_binding_refuses():
+    x = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        fa.fa_fwd_window(x, x, x, 3)
+    with pytest.raises(ValueError, match="dtype"):
+        fa.fa_fwd_window(x.float(), x.float(), x.float(), 3)
