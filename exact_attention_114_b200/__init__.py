@@ -110,6 +110,12 @@ def lib() -> ctypes.CDLL:
             L.fa_fwd_paged_window_workspace_size.restype = sz
             L.fa_fwd_paged_window.argtypes = [ip] + [vp] * 7 + [ip] * 8 + [fl, ip, ip, ip, vp, sz, vp]
             L.fa_fwd_paged_window.restype = ip
+            L.fa_key_weights.argtypes = [ip] + [vp] * 5 + [ip] * 6 + [fl, ip, vp]
+            L.fa_key_weights.restype = ip
+            L.fa_fwd_weights.argtypes = [ip] + [vp] * 7 + [ip] * 6 + [fl, ip, vp]
+            L.fa_fwd_weights.restype = ip
+            L.fa_kv_evict.argtypes = [ip] + [vp] * 8 + [ip] * 6 + [vp]
+            L.fa_kv_evict.restype = ip
             _lib = L
         return _lib
 
@@ -504,6 +510,96 @@ def fa_fwd_paged_window(q, k_cache, v_cache, block_table, seq_lens, window, sink
                                          num_pages, max_pages, _scale(scale, d), int(window), int(sinks),
                                          int(num_splits), _ptr(workspace), ws_bytes, _stream(None)))
     return o, lse
+
+
+def _weights_io(weights, weights_out, k):
+    import torch
+    for t, n in ((weights, "weights"), (weights_out, "weights_out")):
+        if t is not None:
+            _require(t, n, torch.float32, k.shape[:3])
+
+
+def fa_key_weights(q, k, lse, weights=None, weights_out=None, *, causal=False, scale=None, stream=None):
+    """The weight each key receives from the rows of q, added to ``weights`` [B, Hkv, Nk] fp32 (zeros
+    if None): returns ``weights_out`` (a new tensor unless given; it may be ``weights`` itself).
+    ``lse`` is that of the forward of the same q, k, scale and causal flag."""
+    import torch
+    B, Hq, Hkv, Nq, Nk, d = _dims(q, k)
+    dt = _dtype_code(q)
+    _require(q, "q", q.dtype)
+    _require(k, "k", q.dtype)
+    _require(lse, "lse", torch.float32, (B, Hq, Nq))
+    _weights_io(weights, weights_out, k)
+    with _on_device(stream, q, k=k, lse=lse, weights=weights, weights_out=weights_out):
+        if weights_out is None:
+            weights_out = torch.empty((B, Hkv, Nk), dtype=torch.float32, device=q.device)
+        _check(lib().fa_key_weights(dt, _ptr(q), _ptr(k), _ptr(lse), _ptr(weights), _ptr(weights_out), B, Hq, Hkv,
+                                    Nq, Nk, d, _scale(scale, d), int(bool(causal)), _stream(None)))
+    return weights_out
+
+
+def fa_fwd_weights(q, k, v, weights=None, weights_out=None, o=None, lse=None, *, causal=False, scale=None,
+                   stream=None):
+    """Forward that also adds up the weight each key receives: returns (o, lse, weights_out), the last
+    ``weights`` [B, Hkv, Nk] fp32 (zeros if None) plus this call's, in a new tensor unless
+    ``weights_out`` is given (it may be ``weights`` itself)."""
+    import torch
+    B, Hq, Hkv, Nq, Nk, d = _dims(q, k)
+    dt = _dtype_code(q)
+    _check_io(q, k, v, o, q.dtype)
+    _require_lse(lse, B, Hq, Nq)
+    _weights_io(weights, weights_out, k)
+    with _on_device(stream, q, k=k, v=v, weights=weights, weights_out=weights_out, o=o, lse=lse):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+        if weights_out is None:
+            weights_out = torch.empty((B, Hkv, Nk), dtype=torch.float32, device=q.device)
+        _check(lib().fa_fwd_weights(dt, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(weights),
+                                    _ptr(weights_out), B, Hq, Hkv, Nq, Nk, d, _scale(scale, d), int(bool(causal)),
+                                    _stream(None)))
+    return o, lse, weights_out
+
+
+def fa_kv_evict(k, v, weights, keep, recent=0, seq_lens=None, k_out=None, v_out=None, weights_out=None,
+                index_out=None, *, stream=None):
+    """Cuts a KV cache to ``keep`` keys per (batch, kv head): the newest ``recent`` and the heaviest of
+    the others, in order.  k, v [B, Hkv, Nk, d], weights [B, Hkv, Nk] fp32, ``seq_lens`` int32 [B] or
+    None.  Returns (k_out, v_out, weights_out, index_out).  Of a sequence shorter than ``keep`` the rows
+    behind its last key are left as they were; in outputs allocated here they are 0 (index -1)."""
+    import torch
+    dt = _dtype_code(k)
+    if k.dim() != 4 or not k.is_cuda:
+        raise ValueError("k must be a contiguous CUDA tensor [B, Hkv, Nk, d]")
+    B, Hkv, Nk, d = k.shape
+    keep, recent = int(keep), int(recent)
+    _require(k, "k", k.dtype)
+    _require(v, "v", k.dtype, k.shape)
+    _require(weights, "weights", torch.float32, (B, Hkv, Nk))
+    if seq_lens is not None:
+        _require(seq_lens, "seq_lens", torch.int32, (B,))
+    if not 0 <= recent <= keep or keep < 1:
+        raise ValueError(f"keep={keep} must be >= 1 and recent={recent} in [0, keep]")
+    for t, n, dtype, shape in ((k_out, "k_out", k.dtype, (B, Hkv, keep, d)), (v_out, "v_out", k.dtype, (B, Hkv, keep, d)),
+                               (weights_out, "weights_out", torch.float32, (B, Hkv, keep)),
+                               (index_out, "index_out", torch.int32, (B, Hkv, keep))):
+        if t is not None:
+            _require(t, n, dtype, shape)
+    with _on_device(stream, k, v=v, weights=weights, seq_lens=seq_lens, k_out=k_out, v_out=v_out,
+                    weights_out=weights_out, index_out=index_out):
+        def new(shape, dtype, fill):
+            if seq_lens is None and keep <= Nk:   # every row is written
+                return torch.empty(shape, dtype=dtype, device=k.device)
+            return torch.full(shape, fill, dtype=dtype, device=k.device)
+
+        k_out = new((B, Hkv, keep, d), k.dtype, 0) if k_out is None else k_out
+        v_out = new((B, Hkv, keep, d), k.dtype, 0) if v_out is None else v_out
+        weights_out = new((B, Hkv, keep), torch.float32, 0) if weights_out is None else weights_out
+        index_out = new((B, Hkv, keep), torch.int32, -1) if index_out is None else index_out
+        _check(lib().fa_kv_evict(dt, _ptr(k), _ptr(v), _ptr(weights), _ptr(seq_lens), _ptr(k_out), _ptr(v_out),
+                                 _ptr(weights_out), _ptr(index_out), B, Hkv, Nk, d, keep, recent, _stream(None)))
+    return k_out, v_out, weights_out, index_out
 
 
 def fa_check_device_status(stream=None):

@@ -102,7 +102,8 @@ __host__ __device__ __forceinline__ int dec_win_tiles(int Nk, int Nq, int window
 // compiles without the column checks.
 // WIN: sliding window with sinks (causal): only the 64-key tiles that hold a visible key are
 // read, first those of the sinks, then those from the first row's window on.
-template <bool PAGED, typename T = __nv_bfloat16, bool NARROW = false, bool WIN = false>
+// SCORES: the scores are also written out, for the weights that the keys receive.
+template <bool PAGED, typename T = __nv_bfloat16, bool NARROW = false, bool WIN = false, bool SCORES = false>
 __global__ void __launch_bounds__(160, 2)   // two CTAs per SM (shared memory allows exactly two)
     decode_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         DecodeParams p)
@@ -288,6 +289,17 @@ __global__ void __launch_bounds__(160, 2)   // two CTAs per SM (shared memory al
                 __syncwarp();
             }
         }
+        if constexpr (SCORES) {
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int hr = 0; hr < 2; ++hr) {
+                    const int r = g + 8 * hr;
+                    if (r < p.R)
+                        *reinterpret_cast<float2*>(p.scores + ((size_t)kvh * p.R + r) * p.score_stride + key0 +
+                                                   nt * 8 + 2 * tq) = make_float2(s[nt][2 * hr] * sl2, s[nt][2 * hr + 1] * sl2);
+                }
+        }
         // online softmax for rows g (e = 0, 1) and g + 8 (e = 2, 3)
         uint32_t pa[4];
 #pragma unroll
@@ -373,7 +385,7 @@ __global__ void __launch_bounds__(160, 2)   // two CTAs per SM (shared memory al
         }
         const float on = (L > 0.f) ? acc / L : 0.f;
         const float lse = (L > 0.f) ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
-        if (p.splits == 1) {
+        if (p.part_o == nullptr) {   // a single split, final
             const int h = hk * p.G + r / p.Nq, i = r % p.Nq;
             const size_t row = ((size_t)b * p.Hq + h) * p.Nq + i;
             if (dcol < d_io)

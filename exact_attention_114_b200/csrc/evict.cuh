@@ -1,0 +1,521 @@
+// evict.cuh -- eviction from a KV cache by accumulated attention weight.  Per (batch, kv head) and
+// key j the weight is a_j = sum of P_ij over all query rows i of the head's group that have attended
+// so far; a cache over its budget keeps its newest keys and the heaviest of the others.
+//
+//   key_weights_kernel     a_j += sum_i exp(scale q_i.k_j - LSE_i) for any number of rows, from the
+//                          saved LSE (the recomputation of P that the backward does, without its
+//                          gradients)
+//   key_weights_add_kernel adds the sums of a launch whose rows were shared between CTAs
+//   decode_weights_kernel  the same for the split-KV decode, from the scores it leaves behind
+//   evict_select_kernel    the kept keys of each (batch, kv head), in order
+//   evict_gather_kernel    their rows of K and V, moved to the front of a new cache
+#pragma once
+
+#include <type_traits>
+
+#include "sm100.cuh"
+#include "fa_kernels.h"
+
+namespace fa {
+
+struct KeyWeightParams {
+    const float* lse;      // [B, Hq, Nq]
+    const float* w_in;     // [B, Hkv, Nk] or nullptr (zeros)
+    float* w_out;          // [B, Hkv, Nk]
+    float* part;           // [nsp][B * Hkv * Nk] sums of the shares (nsp > 1)
+    int B, Hkv, Nq, Nk;
+    int heads;             // query heads walked one after another: G, or 1 where the group's
+                           // G * Nq rows are one run (row r at position r % Nq)
+    int rows;              // rows of each: Nq, or G * Nq
+    int causal;
+    int nsp;               // CTAs that share a key block's steps
+    float scale_log2;
+};
+
+template <int D>
+struct KeyWCfg {
+    static constexpr int kThreads = 384;
+    static constexpr int kPanels = D / 64;
+    static constexpr int kPanelBytes = 128 * 128;        // 128 rows x 64 elements
+    static constexpr int kTileBytes = kPanels * kPanelBytes;
+    static constexpr int kStages = D == 256 ? 2 : D == 128 ? 4 : 6;
+    static constexpr int kOffK = 0;
+    static constexpr int kOffQ = kTileBytes;
+    static constexpr int kOffVec = kOffQ + kStages * kTileBytes;   // [2 groups][2][128] -LSE log2(e), then positions
+    static constexpr int kOffSum = kOffVec + 2 * 2 * 128 * 8;      // [128] sums of the second group
+    static constexpr int kOffBar = kOffSum + 512;
+    static constexpr int kSmemBytes = kOffBar + 256 + 1024;
+    static constexpr uint32_t kRegsSoftmax = 208, kRegsOther = 88;
+    static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "register split");
+    static_assert((1 + 2 * kStages + 9) * 8 + 8 <= 256, "barrier area");
+    static_assert(kSmemBytes <= 232448, "shared memory per block");
+};
+
+// One CTA per (key block of 128, batch and kv head, share of the steps).  A step is 128 query rows:
+// S^T = K Q^T (keys along TMEM lanes) goes to one of four TMEM buffers, and the two consumer
+// warpgroups take the steps in turn: thread r holds key r, so a step's sum over rows is a sum over
+// the thread's own registers, and no two threads ever add to the same key.  The exponentials bound
+// it (128 x 128 of them against 2 x 128 x 128 x d flops): one pair in four goes to the FMA pipe.
+template <int D, typename T>
+__global__ void __launch_bounds__(384, 1)
+    key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       KeyWeightParams p)
+{
+    using C = KeyWCfg<D>;
+    griddep_launch_dependents();   // the addition of the shares may be scheduled
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+    uint64_t* bar_k = reinterpret_cast<uint64_t*>(smem + C::kOffBar);   // K landed
+    uint64_t* bar_full = bar_k + 1;                 // [kStages] Q slot landed
+    uint64_t* bar_empty = bar_full + C::kStages;    // [kStages] Q slot read
+    uint64_t* bar_s = bar_empty + C::kStages;       // [4] S^T of a step in TMEM
+    uint64_t* bar_free = bar_s + 4;                 // [4] read out (count 4)
+    uint64_t* bar_drain = bar_free + 4;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = warp_id(), lane = lane_id();
+    const int BH = p.B * p.Hkv;
+    // blocks of the first keys, which most rows see, first
+    const int kb = (int)blockIdx.x / (BH * p.nsp);
+    const int kvh = ((int)blockIdx.x % (BH * p.nsp)) / p.nsp;
+    const int sp = (int)blockIdx.x % p.nsp;
+    const int delta = p.Nk - p.Nq;
+    int qb0 = 0, nqb = (p.rows + 127) / 128;
+    if (p.causal) {
+        const int first = kb * 128 - delta;   // first position that sees a key of the block
+        if (first >= p.Nq)
+            nqb = 0;
+        else if (p.rows == p.Nq && first > 0)
+            qb0 = first / 128;
+        nqb = max(0, nqb - qb0);
+    }
+    const long long n_all = (long long)p.heads * nqb;
+    const int it_lo = (int)(sp * n_all / p.nsp);
+    const int n_it = (int)((sp + 1) * n_all / p.nsp) - it_lo;
+    // row tile (tile head, first row) of the CTA's step it
+    auto step = [&](int it, int& th, int& row0) {
+        const int g = it_lo + it;
+        th = kvh * p.heads + g / nqb;
+        row0 = (qb0 + g % nqb) * 128;
+    };
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar_k, 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&bar_full[s], 1);
+            mbar_init(&bar_empty[s], 1);
+        }
+        for (int b = 0; b < 4; ++b) {
+            mbar_init(&bar_s[b], 1);
+            mbar_init(&bar_free[b], 4);
+        }
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp >= 8) {
+        regs_dec<C::kRegsOther>();
+        if (warp == 8 && lane == 0 && n_it > 0) {
+            // ------------------------------------------------------------ TMA producer
+            mbar_arrive_expect_tx(bar_k, C::kTileBytes);
+            for (int pn = 0; pn < C::kPanels; ++pn)
+                tma_load_3d(smem + C::kOffK + pn * C::kPanelBytes, &tmK, bar_k, pn * 64, kb * 128, kvh);
+            int issued = 0;
+            for (int it = 0; it < n_it; ++it) {
+                const int s = it % C::kStages;
+                if (!mbar_wait(&bar_empty[s], (uint32_t)((it / C::kStages) & 1) ^ 1u, abort_flag))
+                    break;
+                int th, row0;
+                step(it, th, row0);
+                mbar_arrive_expect_tx(&bar_full[s], C::kTileBytes);
+                for (int pn = 0; pn < C::kPanels; ++pn)
+                    tma_load_3d(smem + C::kOffQ + s * C::kTileBytes + pn * C::kPanelBytes, &tmQ, &bar_full[s], pn * 64,
+                                row0, th);
+                ++issued;
+            }
+            if (*abort_flag) {
+                // let the loads in flight land before the block exits
+                mbar_wait_limited(bar_k, 0, FA_WAIT_LIMIT_CYCLES);
+                for (int i = max(0, issued - C::kStages); i < issued; ++i)
+                    mbar_wait_limited(&bar_full[i % C::kStages], (uint32_t)((i / C::kStages) & 1), FA_WAIT_LIMIT_CYCLES);
+            }
+        } else if (warp == 9 && n_it > 0) {
+            // ------------------------------------------------------------ MMA issuer
+            const uint32_t id = idesc_f16kind(Elt<T>::kMmaFmt, 128, 128, false, false);
+            const uint64_t dK = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
+            const uint64_t dQ = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+            bool ok = mbar_wait_w(bar_k, 0, abort_flag);
+            for (int it = 0; ok && it < n_it; ++it) {
+                const int s = it % C::kStages, b = it & 3;
+                if (!(ok = mbar_wait_w(&bar_full[s], (uint32_t)((it / C::kStages) & 1), abort_flag)))
+                    break;
+                if (!(ok = mbar_wait_w(&bar_free[b], (uint32_t)((it >> 2) & 1) ^ 1u, abort_flag)))
+                    break;
+                tc_fence_after();
+#pragma unroll 4
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = (uint32_t)((kk >> 2) * C::kPanelBytes + (kk & 3) * 32);
+                    mma_ss_w(tmem + 128u * (uint32_t)b, dK + (uint64_t)(o >> 4),
+                             dQ + (uint64_t)((o + (uint32_t)(s * C::kTileBytes)) >> 4), id, kk > 0 ? 1u : 0u);
+                }
+                mma_commit_w(&bar_empty[s]);
+                mma_commit_w(&bar_s[b]);
+            }
+            if (!ok) {
+                mma_commit_w(bar_drain);
+                mbar_wait_limited(bar_drain, 0, FA_WAIT_LIMIT_CYCLES);
+            }
+        }
+    } else {
+        regs_inc<C::kRegsSoftmax>();
+        // ------------------------------------------------------------ exponentials and sums
+        const int g = warp >> 2, c0 = threadIdx.x & 127;
+        const int r = ((warp & 3) << 5) + lane;            // key within the block = TMEM lane
+        const int key = kb * 128 + r;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        float* vec = reinterpret_cast<float*>(smem + C::kOffVec) + g * 512;   // [2][128] floats, then [2][128] ints
+        int* pos = reinterpret_cast<int*>(vec + 256);
+        const float sl2 = p.scale_log2;
+        const float2 sl22 = make_float2(sl2, sl2);
+        float sum = 0.f;
+        bool ok = true;
+        for (int it = g, u = 0; it < n_it; it += 2, ++u) {
+            int th, row0;
+            step(it, th, row0);
+            // -LSE log2(e) of the step's rows: -inf (P = 0) for rows past the last and rows that see no key
+            const int row = row0 + c0;
+            float nl = -INFINITY;
+            if (row < p.rows) {
+                const float l = __ldg(p.lse + (size_t)th * p.rows + row);
+                nl = (l == -INFINITY) ? -INFINITY : -l * 1.4426950408889634f;
+            }
+            float* v = vec + (u & 1) * 128;
+            int* ps = pos + (u & 1) * 128;
+            v[c0] = nl;
+            ps[c0] = row % p.Nq + delta;
+            named_bar_sync(1 + g, 128);   // also: nobody still reads the buffer of two steps ago
+            const int b = it & 3;
+            ok = mbar_wait(&bar_s[b], (uint32_t)((it >> 2) & 1), abort_flag);
+            ok = named_bar_and(1 + g, 128, ok);   // the four warps go on or stop together
+            if (!ok)
+                break;
+            tc_fence_after();
+            uint32_t sr[128];
+            tmem_ld128(tmem + lane_off + 128u * (uint32_t)b, sr);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bar_free[b]);
+            const float4* v4 = reinterpret_cast<const float4*>(v);
+            // rows whose position does not reach the key: only in the blocks on the diagonal
+            // (every block of a run of short groups)
+            const bool masked = p.causal && (p.rows != p.Nq || row0 + delta < kb * 128 + 127);
+            float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+            auto sums = [&](auto mask_rows) {
+#pragma unroll
+                for (int c = 0; c < 128; c += 4) {
+                    const float4 n4 = v4[c >> 2];
+                    float2 x0 = ffma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl22,
+                                      make_float2(n4.x, n4.y));
+                    float2 x1 = ffma2(make_float2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl22,
+                                      make_float2(n4.z, n4.w));
+                    if (decltype(mask_rows)::value) {
+                        const int4 p4 = *reinterpret_cast<const int4*>(ps + c);
+                        x0.x = p4.x >= key ? x0.x : -INFINITY;
+                        x0.y = p4.y >= key ? x0.y : -INFINITY;
+                        x1.x = p4.z >= key ? x1.x : -INFINITY;
+                        x1.y = p4.w >= key ? x1.y : -INFINITY;
+                    }
+                    a0 = fadd2(a0, make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
+                    a1 = fadd2(a1, make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
+                }
+            };
+            if (masked)
+                sums(std::true_type{});
+            else
+                sums(std::false_type{});
+            sum += (a0.x + a0.y) + (a1.x + a1.y);
+        }
+        // the two groups' sums, in a fixed order
+        float* other = reinterpret_cast<float*>(smem + C::kOffSum);
+        if (g == 1)
+            other[r] = sum;
+        named_bar_sync(3, 256);
+        if (g == 0 && ok && !*abort_flag && key < p.Nk) {
+            const size_t at = (size_t)kvh * p.Nk + key;
+            sum += other[r];
+            if (p.nsp > 1)
+                p.part[(size_t)sp * BH * p.Nk + at] = sum;
+            else
+                p.w_out[at] = (p.w_in ? p.w_in[at] : 0.f) + sum;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// w_out = w_in + the shares' sums, in share order.
+__global__ void __launch_bounds__(256) key_weights_add_kernel(KeyWeightParams p)
+{
+    griddep_wait();   // the sums are complete once key_weights_kernel has finished
+    const size_t n = (size_t)p.B * p.Hkv * p.Nk;
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
+        float s = 0.f;
+        for (int sp = 0; sp < p.nsp; ++sp)
+            s += p.part[(size_t)sp * n + i];
+        p.w_out[i] = (p.w_in ? p.w_in[i] : 0.f) + s;
+    }
+}
+
+// ----------------------------------------------------------------------------
+// decode: the split pass has left its scores (log2 units, -inf where masked) and
+// the partial log-sum-exps.  One block per 256 keys of a (batch, kv head).
+// ----------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) decode_weights_kernel(DecodeParams p)
+{
+    __shared__ float s_lse[16];
+    griddep_wait();
+    const int chunks = (p.Nk + 255) / 256;
+    const int kvh = (int)blockIdx.x / chunks, key = ((int)blockIdx.x % chunks) * 256 + (int)threadIdx.x;
+    const int warp = warp_id(), lane = lane_id();
+    for (int r = warp; r < p.R; r += 8) {
+        // the row's log-sum-exp over its splits (natural units), here in log2 units
+        const size_t base = (size_t)kvh * p.splits * p.R + r;
+        float M = -INFINITY;
+        for (int s = lane; s < p.splits; s += 32)
+            M = fmaxf(M, p.part_lse[base + (size_t)s * p.R]);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        float L = 0.f;
+        if (M != -INFINITY)
+            for (int s = lane; s < p.splits; s += 32)
+                L += __expf(p.part_lse[base + (size_t)s * p.R] - M);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            L += __shfl_xor_sync(0xffffffffu, L, off);
+        if (lane == 0)
+            s_lse[r] = L > 0.f ? (M + __logf(L)) * 1.4426950408889634f : INFINITY;   // P = 0 in a row without keys
+    }
+    __syncthreads();
+    if (key >= p.Nk)
+        return;
+    float sum = 0.f;
+    const float* sc = p.scores + (size_t)kvh * p.R * p.score_stride + key;
+    for (int r = 0; r < p.R; ++r)
+        sum += ex2_approx(sc[(size_t)r * p.score_stride] - s_lse[r]);
+    const size_t at = (size_t)kvh * p.Nk + key;
+    p.w_out[at] = (p.w_in ? p.w_in[at] : 0.f) + sum;
+}
+
+// ----------------------------------------------------------------------------
+// selection
+// ----------------------------------------------------------------------------
+struct EvictParams {
+    const float* w;        // [BH, Nk]
+    const int* seq_lens;   // [B] or nullptr (all Nk)
+    const uint4* k;        // [BH, Nk, d] as 16-byte chunks
+    const uint4* v;
+    uint4* k_out;          // [BH, keep, d]
+    uint4* v_out;
+    float* w_out;          // [BH, keep] or nullptr
+    int* index;            // [BH, keep]
+    int BH, Hkv, Nk, chunks;   // chunks: d * 2 / 16
+    int keep, recent;
+};
+
+// A weight as an unsigned number of the same order: -0 and 0 alike, NaN above all.
+__device__ __forceinline__ uint32_t evict_order(float w)
+{
+    if (w != w)
+        return 0xFFFFFFFFu;
+    const uint32_t u = __float_as_uint(w + 0.f);   // -0 becomes 0
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// One block per (batch, kv head).  Of its n keys the newest `recent` stay, and of the m before them
+// the `need` = keep - recent heaviest: a radix select finds the need-th largest weight T digit by
+// digit (8 bits each, from the highest), then every warp walks its own contiguous part of the keys:
+// a key stays if it is above T, or equal to T with fewer than the remaining number of equal ones
+// before it.  Its place is the number of kept keys before it, so the kept keys stay in order.
+constexpr int kEvictThreads = 1024;
+constexpr int kEvictCache = 48 * 1024;   // keys whose order numbers are held in shared memory
+
+__global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(EvictParams p)
+{
+    extern __shared__ uint32_t s_cache[];
+    __shared__ int s_hist[256];
+    __shared__ int s_gt[32], s_eq[32];
+    __shared__ uint32_t s_digit;
+    __shared__ int s_left;
+    griddep_launch_dependents();
+    const int row = (int)blockIdx.x, warp = warp_id(), lane = lane_id();
+    const int n = p.seq_lens ? max(0, min(__ldg(p.seq_lens + row / p.Hkv), p.Nk)) : p.Nk;
+    const float* w = p.w + (size_t)row * p.Nk;
+    int* index = p.index + (size_t)row * p.keep;
+    float* w_out = p.w_out ? p.w_out + (size_t)row * p.keep : nullptr;
+    if (n <= p.keep) {   // all of them
+        for (int i = (int)threadIdx.x; i < n; i += kEvictThreads) {
+            index[i] = i;
+            if (w_out)
+                w_out[i] = w[i];
+        }
+        return;
+    }
+    const int m = n - p.recent;             // recent <= keep < n
+    const int need = p.keep - p.recent;     // < m
+    const bool cached = m <= kEvictCache;
+    if (cached) {
+        for (int i = (int)threadIdx.x; i < m; i += kEvictThreads)
+            s_cache[i] = evict_order(w[i]);
+        __syncthreads();
+    }
+    auto order = [&](int i) { return cached ? s_cache[i] : evict_order(__ldg(w + i)); };
+
+    uint32_t T = 0xFFFFFFFFu;   // need = 0: nothing is above it, and none of the equal ones stays
+    int left = 0;               // how many of the keys equal to T stay
+    if (need > 0) {
+        T = 0;
+        left = need;
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            for (int i = (int)threadIdx.x; i < 256; i += kEvictThreads)
+                s_hist[i] = 0;
+            __syncthreads();
+            const uint32_t above = shift == 24 ? 0u : (0xFFFFFFFFu << (shift + 8));
+            for (int i0 = 0; i0 < m; i0 += kEvictThreads) {
+                const int i = i0 + (int)threadIdx.x;
+                const uint32_t u = i < m ? order(i) : 0u;
+                const bool in = i < m && (u & above) == (T & above);
+                const int digit = in ? (int)((u >> shift) & 255u) : 256;
+                // one addition per distinct digit of a warp (weights share their exponents)
+                const unsigned same = __match_any_sync(0xffffffffu, digit);
+                if (in && lane == __ffs((int)same) - 1)
+                    atomicAdd(&s_hist[digit], __popc(same));
+            }
+            __syncthreads();
+            if (warp == 0) {
+                // bins from the highest down: lane l holds bins 255 - 8 l .. 248 - 8 l
+                int c[8], sum = 0;
+                for (int k = 0; k < 8; ++k) {
+                    c[k] = s_hist[255 - 8 * lane - k];
+                    sum += c[k];
+                }
+                int before = sum;
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, before, off);
+                    if (lane >= off)
+                        before += x;
+                }
+                before -= sum;   // keys in higher bins than this lane's
+                if (before < left && left <= before + sum) {
+                    int rest = left - before;
+                    int k = 0;
+                    while (rest > c[k])
+                        rest -= c[k++];
+                    s_digit = (uint32_t)(255 - 8 * lane - k);
+                    s_left = rest;
+                }
+            }
+            __syncthreads();
+            T |= s_digit << shift;
+            left = s_left;
+            __syncthreads();
+        }
+    }
+    // counts above and at T in each warp's part
+    const int part = (m + 31) / 32, lo = min(m, warp * part), hi = min(m, lo + part);
+    int gt = 0, eq = 0;
+    for (int i = lo + lane; i < hi; i += 32) {
+        const uint32_t u = order(i);
+        gt += u > T;
+        eq += u == T;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        gt += __shfl_xor_sync(0xffffffffu, gt, off);
+        eq += __shfl_xor_sync(0xffffffffu, eq, off);
+    }
+    if (lane == 0) {
+        s_gt[warp] = gt;
+        s_eq[warp] = eq;
+    }
+    __syncthreads();
+    gt = eq = 0;
+    for (int i = 0; i < warp; ++i) {
+        gt += s_gt[i];
+        eq += s_eq[i];
+    }
+    const unsigned below = (1u << lane) - 1u;
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t u = i < hi ? order(i) : 0u;
+        const bool is_gt = i < hi && u > T, is_eq = i < hi && u == T;
+        const unsigned bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
+        const int eq_before = eq + __popc(be & below);
+        if (is_gt || (is_eq && eq_before < left)) {
+            const int at = gt + __popc(bg & below) + min(eq_before, left);
+            index[at] = i;
+            if (w_out)
+                w_out[at] = w[i];
+        }
+        gt += __popc(bg);
+        eq += __popc(be);
+    }
+    for (int i = m + (int)threadIdx.x; i < n; i += kEvictThreads) {
+        index[need + i - m] = i;
+        if (w_out)
+            w_out[need + i - m] = w[i];
+    }
+}
+
+// The kept rows of K and V, 16 bytes per thread and tensor at a time; bound by HBM (each kept row
+// read and written once).
+constexpr int kGatherItems = 4;
+
+__global__ void __launch_bounds__(256) evict_gather_kernel(EvictParams p)
+{
+    griddep_wait();   // the kept keys' indices are complete once the selection has finished
+    const int per_row = p.keep * p.chunks;                      // chunks of a (batch, kv head)
+    const int blocks = (per_row + 256 * kGatherItems - 1) / (256 * kGatherItems);
+    const int row = (int)(blockIdx.x / (unsigned)blocks), blk = (int)(blockIdx.x % (unsigned)blocks);
+    const int n = p.seq_lens ? max(0, min(__ldg(p.seq_lens + row / p.Hkv), p.Nk)) : p.Nk;
+    const int count = min(n, p.keep) * p.chunks;
+    const size_t in = (size_t)row * p.Nk * p.chunks, out = (size_t)row * per_row;
+    const int* index = p.index + (size_t)row * p.keep;
+    uint4 a[kGatherItems], b[kGatherItems];
+#pragma unroll
+    for (int t = 0; t < kGatherItems; ++t) {
+        const int c = blk * 256 * kGatherItems + t * 256 + (int)threadIdx.x;
+        if (c < count) {
+            const int j = c / p.chunks;
+            const size_t from = in + (size_t)index[j] * p.chunks + (c - j * p.chunks);
+            a[t] = __ldcs(p.k + from);
+            b[t] = __ldcs(p.v + from);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kGatherItems; ++t) {
+        const int c = blk * 256 * kGatherItems + t * 256 + (int)threadIdx.x;
+        if (c < count) {
+            p.k_out[out + c] = a[t];
+            p.v_out[out + c] = b[t];
+        }
+    }
+}
+
+}  // namespace fa

@@ -23,6 +23,7 @@
 
 #include "bwd.cuh"
 #include "decode.cuh"
+#include "evict.cuh"
 #include "fa_kernels.h"
 #include "fp8.cuh"
 #include "fwd.cuh"
@@ -741,7 +742,17 @@ int decode_splits(int B, int Hkv, int Nk, int requested)
 struct DecodePlan {
     int splits, chunk;
     size_t o_bytes, lse_bytes;
-    size_t total() const { return splits > 1 ? align256(o_bytes) + align256(lse_bytes) : 0; }
+    bool partial = false;   // partial results even of a single split
+    bool partials() const { return splits > 1 || partial; }
+    size_t total() const { return partials() ? align256(o_bytes) + align256(lse_bytes) : 0; }
+};
+
+// The keys' weights that a decode adds up (fa_fwd_weights)
+struct DecodeWeights {
+    const float* in;
+    float* out;
+    float* scores;
+    int stride;
 };
 
 DecodePlan decode_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d, int requested)
@@ -767,7 +778,7 @@ struct PagedDesc {
 template <typename T>
 fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
                             int Hkv, int Nq, int Nk, int d, float scale, int causal, const DecodePlan& pl, void* ws,
-                            cudaStream_t stream, const PagedDesc* pg, const Window* win)
+                            cudaStream_t stream, const PagedDesc* pg, const Window* win, const DecodeWeights* dw)
 {
     using C = fa::DecCfg;
     CUtensorMap mk, mv;
@@ -784,15 +795,17 @@ fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o
     if (win)
         kern = d < 128 ? (pg ? fa::decode_split_kernel<true, T, true, true> : fa::decode_split_kernel<false, T, true, true>)
                        : (pg ? fa::decode_split_kernel<true, T, false, true> : fa::decode_split_kernel<false, T, false, true>);
+    if (dw)
+        kern = d < 128 ? fa::decode_split_kernel<false, T, true, false, true> : fa::decode_split_kernel<false, T, false, false, true>;
     if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
-    fa::DecodeParams p;
+    fa::DecodeParams p = {};
     p.q = q;
     p.k = k;
     p.v = v;
     p.o = o;
     p.lse = lse;
-    p.part_o = pl.splits > 1 ? static_cast<float*>(ws) : nullptr;
-    p.part_lse = pl.splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(ws) + align256(pl.o_bytes)) : nullptr;
+    p.part_o = pl.partials() ? static_cast<float*>(ws) : nullptr;
+    p.part_lse = pl.partials() ? reinterpret_cast<float*>(static_cast<char*>(ws) + align256(pl.o_bytes)) : nullptr;
     p.B = B;
     p.Hq = Hq;
     p.Hkv = Hkv;
@@ -811,14 +824,26 @@ fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o
     p.max_pages = pg ? pg->max_pages : 0;
     p.window = win ? win->window : 0;
     p.sinks = win ? win->sinks : 0;
+    if (dw) {
+        p.scores = dw->scores;
+        p.score_stride = dw->stride;
+        p.w_in = dw->in;
+        p.w_out = dw->out;
+    }
     const long long grid = (long long)B * Hkv * pl.splits;
     kern<<<(unsigned)grid, C::kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
     if ((st = check_launch("decode_split_kernel launch")) != FA_OK) return st;
-    if (pl.splits > 1) {
+    if (pl.partials()) {
         const long long rows = (long long)B * Hkv * p.R;
         if ((st = launch_dependent("decode_combine_kernel launch", fa::decode_combine_kernel<T>,
                                    dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, p)) != FA_OK)
             return st;
+    }
+    if (dw) {
+        // launched plainly: the scores are two kernels back
+        const long long blocks = (long long)B * Hkv * ((Nk + 255) / 256);
+        fa::decode_weights_kernel<<<(unsigned)blocks, 256, 0, stream>>>(p);
+        return check_launch("decode_weights_kernel launch");
     }
     return FA_OK;
 }
@@ -826,12 +851,13 @@ fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o
 fa_status_t launch_decode(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
                           int Nq, int Nk, int d, float scale, int causal, const DecodePlan& pl, void* ws,
                           cudaStream_t stream, const PagedDesc* pg = nullptr, int dtype = FA_DTYPE_BF16,
-                          const Window* win = nullptr)
+                          const Window* win = nullptr, const DecodeWeights* dw = nullptr)
 {
     if (dtype == FA_DTYPE_FP16)
-        return launch_decode_t<__half>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, stream, pg, win);
+        return launch_decode_t<__half>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, stream, pg, win,
+                                       dw);
     return launch_decode_t<__nv_bfloat16>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, stream, pg,
-                                          win);
+                                          win, dw);
 }
 
 // Keys of the longest list of visible tiles that a windowed decode may meet: Nk keys in a dense
@@ -1156,6 +1182,117 @@ fa_status_t bwd_win_dispatch(const fa::BwdParams& p, const void* q, const void* 
     if (kd == 128)
         return launch_bwd<128, true, T, true>(p, q, k, v, dout, s);
     return launch_bwd<64, true, T, true>(p, q, k, v, dout, s);
+}
+
+// ---------------------------------------------------------------------------
+// weights that the keys receive, and eviction
+// ---------------------------------------------------------------------------
+template <int D, typename T>
+fa_status_t launch_key_weights(const void* q, const void* k, fa::KeyWeightParams p, int G, int d, cudaStream_t stream)
+{
+    using C = fa::KeyWCfg<D>;
+    CUtensorMap mq, mk;
+    fa_status_t st;
+    const uint64_t BH = (uint64_t)p.B * p.Hkv;
+    // few rows per head: the group's rows as one run (a kv head's query heads are consecutive)
+    p.heads = p.Nq < 128 ? 1 : G;
+    p.rows = p.Nq < 128 ? G * p.Nq : p.Nq;
+    if ((st = make_map(&mq, q, d, p.rows, BH * p.heads, 128, tma_type<T>())) != FA_OK) return st;
+    if ((st = make_map(&mk, k, d, p.Nk, BH, 128, tma_type<T>())) != FA_OK) return st;
+    auto kern = fa::key_weights_kernel<D, T>;
+    if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
+    // Enough CTAs to fill the SMs a few times over, as long as each keeps 16 steps
+    const long long units = (long long)BH * ((p.Nk + 127) / 128), steps = (long long)p.heads * ((p.rows + 127) / 128);
+    const int sms = sm_count();
+    p.nsp = 1;
+    while (p.nsp < 64 && units * p.nsp < 3LL * sms && steps >= 32LL * p.nsp)
+        p.nsp *= 2;
+    void* ws = nullptr;
+    if (p.nsp > 1) {
+        cudaError_t e = scratch_alloc(&ws, (size_t)p.nsp * BH * p.Nk * 4, stream);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "scratch allocation (key weight sums)");
+        p.part = static_cast<float*>(ws);
+    }
+    kern<<<(unsigned)(units * p.nsp), C::kThreads, C::kSmemBytes, stream>>>(mq, mk, p);
+    st = check_launch("key_weights_kernel launch");
+    if (ws) {
+        if (st == FA_OK) {
+            const size_t blocks = std::min<size_t>((BH * p.Nk + 255) / 256, (size_t)sms * 8);
+            st = launch_dependent("key_weights_add_kernel launch", fa::key_weights_add_kernel, dim3((unsigned)blocks),
+                                  dim3(256), 0, stream, p);
+        }
+        cudaError_t e = cudaFreeAsync(ws, stream);
+        if (e != cudaSuccess && st == FA_OK)
+            st = cuda_fail(e, "cudaFreeAsync");
+    }
+    return st;
+}
+
+template <typename T>
+fa_status_t key_weights_t(const void* q, const void* k, const fa::KeyWeightParams& p, int G, int d, cudaStream_t s)
+{
+    if (kernel_d(d) == 256)
+        return launch_key_weights<256, T>(q, k, p, G, d, s);
+    if (kernel_d(d) == 128)
+        return launch_key_weights<128, T>(q, k, p, G, d, s);
+    return launch_key_weights<64, T>(q, k, p, G, d, s);
+}
+
+fa_status_t key_weights(int dtype, const void* q, const void* k, const float* lse, const float* w_in, float* w_out,
+                        int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, int causal, cudaStream_t s)
+{
+    fa::KeyWeightParams p = {};
+    p.lse = lse;
+    p.w_in = w_in;
+    p.w_out = w_out;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.Nq = Nq;
+    p.Nk = Nk;
+    p.causal = causal;
+    p.scale_log2 = scale * kLog2e;
+    return dtype == FA_DTYPE_FP16 ? key_weights_t<__half>(q, k, p, Hq / Hkv, d, s)
+                                  : key_weights_t<__nv_bfloat16>(q, k, p, Hq / Hkv, d, s);
+}
+
+fa_status_t check_float(const void* p, const char* name, bool may_be_null)
+{
+    if (!p && may_be_null)
+        return FA_OK;
+    if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) {
+        set_error("%s must be non-NULL and 4-byte aligned", name);
+        return FA_ERR_INVALID_ARGUMENT;
+    }
+    return FA_OK;
+}
+
+fa_status_t check_dtype(int dtype)
+{
+    if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_FP16) {
+        set_error("dtype=%d is not FA_DTYPE_BF16 or FA_DTYPE_FP16", dtype);
+        return FA_ERR_INVALID_ARGUMENT;
+    }
+    return FA_OK;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
+// weights_in is weights_out or apart from it
+fa_status_t check_weights(const float* in, const float* out, size_t n)
+{
+    fa_status_t st;
+    if ((st = check_float(in, "weights_in", true)) || (st = check_float(out, "weights_out", false)))
+        return st;
+    if (in != out && overlap(in, n * 4, out, n * 4)) {
+        set_error("weights_in and weights_out overlap without being the same");
+        return FA_ERR_INVALID_ARGUMENT;
+    }
+    return FA_OK;
 }
 
 // ---------------------------------------------------------------------------
@@ -1721,6 +1858,141 @@ fa_status_t fa_fwd_paged_window(fa_dtype_t dtype, const void* q, const void* k_c
     const int w[2] = {window, sinks};
     return paged_entry((int)dtype, q, k_cache, v_cache, block_table, seq_lens, o, lse, B, Hq, Hkv, Nq, d, page_size,
                        num_pages, max_pages_per_seq, scale, 1, num_splits, workspace, workspace_bytes, stream, w);
+}
+
+fa_status_t fa_key_weights(fa_dtype_t dtype, const void* q, const void* k, const float* lse, const float* weights_in,
+                           float* weights_out, int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, int causal,
+                           void* stream)
+{
+    t_error.clear();
+    fa_status_t st;
+    if ((st = check_dtype((int)dtype)) || (st = check_ptr(q, "q")) || (st = check_ptr(k, "k")) ||
+        (st = check_float(lse, "lse", false)) || (st = check_shape(B, Hq, Hkv, Nq, Nk, d, scale, causal)) ||
+        (st = check_weights(weights_in, weights_out, (size_t)B * Hkv * Nk)))
+        return st;
+    return key_weights((int)dtype, q, k, lse, weights_in, weights_out, B, Hq, Hkv, Nq, Nk, d, scale, causal,
+                       static_cast<cudaStream_t>(stream));
+}
+
+fa_status_t fa_fwd_weights(fa_dtype_t dtype, const void* q, const void* k, const void* v, void* o, float* lse,
+                           const float* weights_in, float* weights_out, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                           float scale, int causal, void* stream)
+{
+    t_error.clear();
+    fa_status_t st;
+    if ((st = check_dtype((int)dtype)) || (st = check_ptr(q, "q")) || (st = check_ptr(k, "k")) ||
+        (st = check_ptr(v, "v")) || (st = check_ptr(o, "o")) || (st = check_float(lse, "lse", true)) ||
+        (st = check_shape(B, Hq, Hkv, Nq, Nk, d, scale, causal)) ||
+        (st = check_weights(weights_in, weights_out, (size_t)B * Hkv * Nk)))
+        return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void* ws = nullptr;
+    if (decode_shape(Hq, Hkv, Nq, d)) {
+        DecodePlan pl = decode_plan(B, Hq, Hkv, Nq, Nk, d, 0);
+        pl.partial = true;
+        const int stride = (Nk + 63) / 64 * 64;
+        const size_t need = pl.total() + (size_t)B * Hq * Nq * stride * 4;
+        cudaError_t e = scratch_alloc(&ws, need, s);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "scratch allocation (decode partials and scores)");
+        const DecodeWeights dw{weights_in, weights_out, reinterpret_cast<float*>(static_cast<char*>(ws) + pl.total()),
+                               stride};
+        st = launch_decode(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, s, nullptr, (int)dtype,
+                           nullptr, &dw);
+    } else {
+        float* l = lse;
+        if (!l) {
+            cudaError_t e = scratch_alloc(&ws, (size_t)B * Hq * Nq * 4, s);
+            if (e != cudaSuccess)
+                return cuda_fail(e, "scratch allocation (log-sum-exp)");
+            l = static_cast<float*>(ws);
+        }
+        st = fwd_tiled((int)dtype, q, k, v, o, l, B, Hq, Hkv, Nq, Nk, d, scale, causal, s);
+        if (st == FA_OK)
+            st = key_weights((int)dtype, q, k, l, weights_in, weights_out, B, Hq, Hkv, Nq, Nk, d, scale, causal, s);
+    }
+    if (ws) {
+        cudaError_t e = cudaFreeAsync(ws, s);
+        if (e != cudaSuccess && st == FA_OK)
+            st = cuda_fail(e, "cudaFreeAsync");
+    }
+    return st;
+}
+
+fa_status_t fa_kv_evict(fa_dtype_t dtype, const void* k, const void* v, const float* weights, const int* seq_lens,
+                        void* k_out, void* v_out, float* weights_out, int* index_out, int B, int Hkv, int Nk, int d,
+                        int keep, int recent, void* stream)
+{
+    t_error.clear();
+    fa_status_t st;
+    if ((st = check_dtype((int)dtype)) || (st = check_ptr(k, "k")) || (st = check_ptr(v, "v")) ||
+        (st = check_float(weights, "weights", false)) || (st = check_float(seq_lens, "seq_lens", true)) ||
+        (st = check_ptr(k_out, "k_out")) || (st = check_ptr(v_out, "v_out")) ||
+        (st = check_float(weights_out, "weights_out", true)) || (st = check_float(index_out, "index_out", true)) ||
+        (st = check_shape(B, Hkv, Hkv, 1, Nk, d, 1.f, 0)))
+        return st;
+    if (keep < 1 || recent < 0 || recent > keep) {
+        set_error("keep=%d must be >= 1 and recent=%d in [0, keep]", keep, recent);
+        return FA_ERR_INVALID_ARGUMENT;
+    }
+    const size_t BH = (size_t)B * Hkv, in_bytes = BH * Nk * d * 2, out_bytes = BH * keep * d * 2;
+    if ((long long)keep * (d / 8) > (1ll << 31) - 4096 ||
+        BH * (((size_t)keep * (d / 8) + 1023) / 1024) > (size_t)(1u << 31) - 1) {
+        set_error("keep=%d is too large for 32-bit indices", keep);
+        return FA_ERR_UNSUPPORTED;
+    }
+    const struct {
+        const void* p;
+        size_t n;
+        bool out;
+    } bufs[] = {{k, in_bytes, false},      {v, in_bytes, false},       {weights, BH * Nk * 4, false}, {seq_lens, (size_t)B * 4, false},
+                {k_out, out_bytes, true},  {v_out, out_bytes, true},   {weights_out, BH * keep * 4, true},
+                {index_out, BH * keep * 4, true}};
+    for (int i = 0; i < 8; ++i)
+        for (int j = i + 1; j < 8; ++j)
+            if ((bufs[i].out || bufs[j].out) && overlap(bufs[i].p, bufs[i].n, bufs[j].p, bufs[j].n)) {
+                set_error("an output overlaps an input or another output");
+                return FA_ERR_INVALID_ARGUMENT;
+            }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void* ws = nullptr;
+    if (!index_out) {
+        cudaError_t e = scratch_alloc(&ws, BH * keep * 4, s);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "scratch allocation (kept indices)");
+    }
+    fa::EvictParams p = {};
+    p.w = weights;
+    p.seq_lens = seq_lens;
+    p.k = static_cast<const uint4*>(k);
+    p.v = static_cast<const uint4*>(v);
+    p.k_out = static_cast<uint4*>(k_out);
+    p.v_out = static_cast<uint4*>(v_out);
+    p.w_out = weights_out;
+    p.index = index_out ? index_out : static_cast<int*>(ws);
+    p.BH = (int)BH;
+    p.Hkv = Hkv;
+    p.Nk = Nk;
+    p.chunks = d / 8;
+    p.keep = keep;
+    p.recent = recent;
+    const int cache = std::min(Nk, fa::kEvictCache) * 4;
+    st = ensure_smem(reinterpret_cast<const void*>(&fa::evict_select_kernel), fa::kEvictCache * 4);
+    if (st == FA_OK) {
+        fa::evict_select_kernel<<<(unsigned)BH, fa::kEvictThreads, cache, s>>>(p);
+        st = check_launch("evict_select_kernel launch");
+    }
+    if (st == FA_OK) {
+        const size_t per = ((size_t)keep * p.chunks + 256 * fa::kGatherItems - 1) / (256 * fa::kGatherItems);
+        st = launch_dependent("evict_gather_kernel launch", fa::evict_gather_kernel, dim3((unsigned)(BH * per)), dim3(256),
+                              0, s, p);
+    }
+    if (ws) {
+        cudaError_t e = cudaFreeAsync(ws, s);
+        if (e != cudaSuccess && st == FA_OK)
+            st = cuda_fail(e, "cudaFreeAsync");
+    }
+    return st;
 }
 
 fa_status_t fa_check_device_status(void* stream)

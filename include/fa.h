@@ -364,6 +364,47 @@ fa_status_t fa_fwd_paged_window(fa_dtype_t dtype, const void* q, const void* k_c
                                 size_t workspace_bytes, void* stream);
 
 /*
+ * The weight that each key has received, for eviction from a KV cache.  Per
+ * (batch, kv head) and key j, over all query rows i of the group's Hq / Hkv
+ * heads:
+ *     weights_out[j] = weights_in[j] + sum_i exp(scale q_i.k_j - lse_i)
+ *   weights_in, weights_out: [B, Hkv, Nk] fp32; weights_in NULL counts as zeros,
+ *   and may be weights_out itself (added up in place) but not overlap it in
+ *   another way.  Sums are taken in fp32 in a fixed order (they repeat bitwise).
+ *   Rows that see no key (lse = -inf) add nothing.
+ * fa_key_weights takes the lse of an earlier forward of the same q, k, scale and
+ * causal flag.  fa_fwd_weights is fa_fwd_ex that also adds the weights: in decode
+ * shapes (Nq * Hq / Hkv <= 16, d <= 128) the split pass leaves its scores (fp32,
+ * in stream-ordered scratch of B * Hq * Nq * Nk values) and K is read once;
+ * other shapes run the forward and then fa_key_weights.  lse may be NULL there.
+ */
+fa_status_t fa_key_weights(fa_dtype_t dtype, const void* q, const void* k, const float* lse,
+                           const float* weights_in, float* weights_out, int B, int Hq, int Hkv, int Nq, int Nk,
+                           int d, float scale, int causal, void* stream);
+fa_status_t fa_fwd_weights(fa_dtype_t dtype, const void* q, const void* k, const void* v, void* o, float* lse,
+                           const float* weights_in, float* weights_out, int B, int Hq, int Hkv, int Nq, int Nk,
+                           int d, float scale, int causal, void* stream);
+
+/*
+ * Eviction from a KV cache: of each (batch, kv head)'s keys the newest `recent`
+ * stay and, of the ones before them, those with the largest weights, `keep` in
+ * all, in their order.  Of equal weights the one with the lower index stays
+ * first; NaN counts as larger than any number, -0 as 0.
+ *   k, v [B, Hkv, Nk, d] 16-bit, weights [B, Hkv, Nk] fp32 (read only).
+ *   seq_lens: int32 [B] (device) or NULL; sequence b holds its first seq_lens[b]
+ *   keys (clamped to 0 .. Nk), all Nk of them without it.
+ *   k_out, v_out [B, Hkv, keep, d], weights_out [B, Hkv, keep] fp32 (or NULL),
+ *   index_out [B, Hkv, keep] int32 (or NULL): the kept keys' rows, weights and
+ *   old indices.  A sequence with n <= keep keys keeps them all; rows from
+ *   min(n, keep) on are left as they were in every output.
+ *   keep >= 1 (it may exceed Nk), 0 <= recent <= keep.  The outputs must not
+ *   overlap the inputs or one another.
+ */
+fa_status_t fa_kv_evict(fa_dtype_t dtype, const void* k, const void* v, const float* weights,
+                        const int* seq_lens, void* k_out, void* v_out, float* weights_out, int* index_out, int B,
+                        int Hkv, int Nk, int d, int keep, int recent, void* stream);
+
+/*
  * Reads and clears the device status word of the current device.  Synchronises
  * `stream` (the only call that does).  Returns FA_OK; FA_ERR_SLOT_CONFLICT if a
  * tiled forward found its tile-counter slot held by another launch since the
