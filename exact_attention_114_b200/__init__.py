@@ -116,6 +116,10 @@ def lib() -> ctypes.CDLL:
             L.fa_fwd_weights.restype = ip
             L.fa_kv_evict.argtypes = [ip] + [vp] * 8 + [ip] * 6 + [vp]
             L.fa_kv_evict.restype = ip
+            L.fa_fwd_prefix_workspace_size.argtypes = [ip] * 7
+            L.fa_fwd_prefix_workspace_size.restype = sz
+            L.fa_fwd_prefix.argtypes = [ip] + [vp] * 8 + [ip] * 7 + [fl, ip, vp, sz, vp]
+            L.fa_fwd_prefix.restype = ip
             _lib = L
         return _lib
 
@@ -509,6 +513,40 @@ def fa_fwd_paged_window(q, k_cache, v_cache, block_table, seq_lens, window, sink
                                          _ptr(seq_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, d, page_size,
                                          num_pages, max_pages, _scale(scale, d), int(window), int(sinks),
                                          int(num_splits), _ptr(workspace), ws_bytes, _stream(None)))
+    return o, lse
+
+
+def fa_fwd_prefix_workspace_size(B, Hq, Hkv, Nq, Np, Ns, d) -> int:
+    return int(lib().fa_fwd_prefix_workspace_size(B, Hq, Hkv, Nq, Np, Ns, d))
+
+
+def fa_fwd_prefix(q, k_prefix, v_prefix, k, v, seq_lens=None, o=None, lse=None, *, causal=False, scale=None,
+                  workspace=None, stream=None):
+    """Forward of a batch whose sequences share a prefix: q [B, Hq, Nq, d], k_prefix / v_prefix
+    [Hkv, Np, d], own keys k / v [B, Hkv, Ns, d] of which sequence b holds the first
+    ``seq_lens[b]`` (int32 [B]; all without it).  Returns (o, lse), as ``fa_fwd`` on the
+    concatenated keys would."""
+    import torch
+    B, Hq, Hkv, Nq, Ns, d = _dims(q, k)
+    dt = _dtype_code(q)
+    _check_io(q, k, v, o, q.dtype)
+    if k_prefix.dim() != 3 or k_prefix.shape[0] != Hkv or k_prefix.shape[2] != d:
+        raise ValueError(f"k_prefix has shape {tuple(k_prefix.shape)}, expected ({Hkv}, Np, {d})")
+    _require(k_prefix, "k_prefix", q.dtype)
+    _require(v_prefix, "v_prefix", q.dtype, k_prefix.shape)
+    if seq_lens is not None:
+        _require(seq_lens, "seq_lens", torch.int32, (B,))
+    _require_lse(lse, B, Hq, Nq)
+    ws_bytes = _ws_bytes(workspace)
+    with _on_device(stream, q, k_prefix=k_prefix, v_prefix=v_prefix, k=k, v=v, seq_lens=seq_lens, o=o, lse=lse,
+                    workspace=workspace):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+        _check(lib().fa_fwd_prefix(dt, _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), _ptr(seq_lens),
+                                   _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, k_prefix.shape[1], Ns, d, _scale(scale, d),
+                                   int(bool(causal)), _ptr(workspace), ws_bytes, _stream(None)))
     return o, lse
 
 

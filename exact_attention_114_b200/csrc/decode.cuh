@@ -103,7 +103,9 @@ __host__ __device__ __forceinline__ int dec_win_tiles(int Nk, int Nq, int window
 // WIN: sliding window with sinks (causal): only the 64-key tiles that hold a visible key are
 // read, first those of the sinks, then those from the first row's window on.
 // SCORES: the scores are also written out, for the weights that the keys receive.
-template <bool PAGED, typename T = __nv_bfloat16, bool NARROW = false, bool WIN = false, bool SCORES = false>
+// LENS: a padded dense cache, sequence b holding its first seq_lens[b] keys.
+template <bool PAGED, typename T = __nv_bfloat16, bool NARROW = false, bool WIN = false, bool SCORES = false,
+          bool LENS = false>
 __global__ void __launch_bounds__(160, 2)   // two CTAs per SM (shared memory allows exactly two)
     decode_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         DecodeParams p)
@@ -123,7 +125,9 @@ __global__ void __launch_bounds__(160, 2)   // two CTAs per SM (shared memory al
     const int kvh = (int)blockIdx.x / p.splits;     // b * Hkv + kv head
     const int b = kvh / p.Hkv, hk = kvh % p.Hkv;
     // keys of this sequence (a paged sequence's own length, clamped to what its table can hold)
-    const int Nk_b = PAGED ? max(0, min(__ldg(p.seq_lens + b), p.max_pages * p.page_size)) : p.Nk;
+    const int Nk_b = PAGED  ? max(0, min(__ldg(p.seq_lens + b), p.max_pages * p.page_size))
+                     : LENS ? max(0, min(__ldg(p.seq_lens + b), p.Nk))
+                            : p.Nk;
     int k_begin = split * p.chunk;
     int k_end = min(Nk_b, k_begin + p.chunk);
     int n_tiles = k_end > k_begin ? (k_end - k_begin + C::kKeys - 1) / C::kKeys : 0;
@@ -275,13 +279,13 @@ __global__ void __launch_bounds__(160, 2)   // two CTAs per SM (shared memory al
                 if (key > lim[e >> 1] || (WIN && key < low[e >> 1] && key >= p.sinks))
                     s[nt][e] = -INFINITY;
             }
-        if constexpr (WIN) {
+        if constexpr (WIN || LENS) {
             // V rows of keys that no row sees (between the sinks and the window, or past the
-            // sequence in its last page) are zeroed: whatever they hold, 0 * V adds nothing
-            if (key0 + 16 > Nk_b || (key0 < win_lo && key0 + 16 > p.sinks)) {
+            // sequence in its last page or in the padding) are zeroed: whatever they hold, 0 * V adds nothing
+            if (key0 + 16 > Nk_b || (WIN && key0 < win_lo && key0 + 16 > p.sinks)) {
                 for (int i = lane; i < 256; i += 32) {
                     const int key = key0 + (i >> 4);
-                    if (key >= Nk_b || (key >= p.sinks && key < win_lo))
+                    if (key >= Nk_b || (WIN && key >= p.sinks && key < win_lo))
                         *reinterpret_cast<uint4*>(smem + C::kOffRing + slot * 2 * C::kTileBytes + C::kTileBytes +
                                                   dec_tile_off(key_w + (i >> 4), i & 15)) = make_uint4(0u, 0u, 0u, 0u);
                 }

@@ -476,13 +476,14 @@ fa_status_t fwd_tile_counter(unsigned** ctr, unsigned* tag)
 
 // The tiled forward's launch: with a key split (p.kv_split > 1) the shares' fp32 partials
 // go to stream-ordered scratch and fwd_combine_kernel merges them into o / lse.
-template <typename T, bool WIN = false, typename Kern>
+template <typename T, int MODE = fa::kFwdPlain, typename Kern>
 fa_status_t launch_fwd_tiles(Kern kern, int threads, int smem, const CUtensorMap& mq, const CUtensorMap& mk,
                              const CUtensorMap& mv, fa::FwdParams& p, cudaStream_t stream,
-                             bool after_kernel = false, const fa::FwdExtra<WIN>& ex = fa::FwdExtra<WIN>{})
+                             bool after_kernel = false, const fa::FwdExtra<MODE>& ex = fa::FwdExtra<MODE>{})
 {
     void* ws = nullptr;
-    if (p.kv_split > 1) {
+    const bool merge = p.kv_split > 1 && !p.partial;
+    if (merge) {
         // indexed by tile head and share: [n_bh][kv_split][rows] (only split units' rows used)
         const size_t rows = (size_t)p.n_bh * p.kv_split * p.rows;
         const size_t o_bytes = align256(rows * p.d_io * 4);
@@ -493,7 +494,7 @@ fa_status_t launch_fwd_tiles(Kern kern, int threads, int smem, const CUtensorMap
         p.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + o_bytes);
     }
     fa_status_t st;
-    if (after_kernel && p.kv_split <= 1) {
+    if (after_kernel && !merge) {
         // straight after a kernel of the same call (the e4m3 V transpose)
         st = launch_dependent("fwd_kernel launch", kern, dim3(fwd_grid(p)), dim3(threads), (size_t)smem, stream,
                               mq, mk, mv, ex, p);
@@ -501,7 +502,7 @@ fa_status_t launch_fwd_tiles(Kern kern, int threads, int smem, const CUtensorMap
         kern<<<fwd_grid(p), threads, smem, stream>>>(mq, mk, mv, ex, p);
         st = check_launch("fwd_kernel launch");
     }
-    if (p.kv_split > 1) {
+    if (merge) {
         if (st == FA_OK) {
             const long long rows = (long long)p.n_bh * p.rows;
             st = launch_dependent("fwd_combine_kernel launch", fa::fwd_combine_kernel<T>,
@@ -652,7 +653,7 @@ fa_status_t launch_fwd_win(const void* q, const void* k, const void* v, void* o,
 {
     using C = fa::FwdCfg<D>;
     CUtensorMap mq, mk, mv;
-    fa::FwdExtra<true> ex;
+    fa::FwdExtra<fa::kFwdWindow> ex;
     fa_status_t st;
     const FwdGeom g = fwd_geom(B, Hq, Hkv, Nq, d);
     const uint64_t kvh = (uint64_t)B * Hkv;
@@ -676,7 +677,8 @@ fa_status_t launch_fwd_win(const void* q, const void* k, const void* v, void* o,
         fa::fwd_win_blocks(pr * 128 * C::kTiles, C::kTiles, g.rows, Nq, Nk, w.window, w.sinks, 128 * full + rem, lo, nb);
         return std::max(nb[0], nb[1]);
     });
-    auto kern = sp.shares > 1 ? fa::fwd_kernel<D, true, T, false, true, true> : fa::fwd_kernel<D, true, T, false, false, true>;
+    auto kern = sp.shares > 1 ? fa::fwd_kernel<D, true, T, false, true, fa::kFwdWindow>
+                              : fa::fwd_kernel<D, true, T, false, false, fa::kFwdWindow>;
     if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
     fa::FwdParams p = fwd_params(g, o, lse, B, Hq, Hkv, Nq, Nk, d, scale * kLog2e, sp);
     p.window = w.window;
@@ -685,7 +687,7 @@ fa_status_t launch_fwd_win(const void* q, const void* k, const void* v, void* o,
     p.sink_rem = rem;
     if ((st = fwd_tile_counter(&p.tile_ctr, &p.tile_tag)) != FA_OK)
         return st;
-    return launch_fwd_tiles<T, true>(kern, C::kThreads, C::kSmemBytes, mq, mk, mv, p, stream, false, ex);
+    return launch_fwd_tiles<T, fa::kFwdWindow>(kern, C::kThreads, C::kSmemBytes, mq, mk, mv, p, stream, false, ex);
 }
 
 template <typename T>
@@ -778,7 +780,8 @@ struct PagedDesc {
 template <typename T>
 fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
                             int Hkv, int Nq, int Nk, int d, float scale, int causal, const DecodePlan& pl, void* ws,
-                            cudaStream_t stream, const PagedDesc* pg, const Window* win, const DecodeWeights* dw)
+                            cudaStream_t stream, const PagedDesc* pg, const Window* win, const DecodeWeights* dw,
+                            const int* lens, bool merge)
 {
     using C = fa::DecCfg;
     CUtensorMap mk, mv;
@@ -797,6 +800,9 @@ fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o
                        : (pg ? fa::decode_split_kernel<true, T, false, true> : fa::decode_split_kernel<false, T, false, true>);
     if (dw)
         kern = d < 128 ? fa::decode_split_kernel<false, T, true, false, true> : fa::decode_split_kernel<false, T, false, false, true>;
+    if (lens)
+        kern = d < 128 ? fa::decode_split_kernel<false, T, true, false, false, true>
+                       : fa::decode_split_kernel<false, T, false, false, false, true>;
     if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
     fa::DecodeParams p = {};
     p.q = q;
@@ -819,7 +825,7 @@ fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o
     p.d_io = d;
     p.scale_log2 = scale * kLog2e;
     p.block_table = pg ? pg->block_table : nullptr;
-    p.seq_lens = pg ? pg->seq_lens : nullptr;
+    p.seq_lens = pg ? pg->seq_lens : lens;
     p.page_size = pg ? pg->page_size : 0;
     p.max_pages = pg ? pg->max_pages : 0;
     p.window = win ? win->window : 0;
@@ -833,7 +839,7 @@ fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o
     const long long grid = (long long)B * Hkv * pl.splits;
     kern<<<(unsigned)grid, C::kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
     if ((st = check_launch("decode_split_kernel launch")) != FA_OK) return st;
-    if (pl.partials()) {
+    if (pl.partials() && merge) {
         const long long rows = (long long)B * Hkv * p.R;
         if ((st = launch_dependent("decode_combine_kernel launch", fa::decode_combine_kernel<T>,
                                    dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, p)) != FA_OK)
@@ -855,9 +861,9 @@ fa_status_t launch_decode(const void* q, const void* k, const void* v, void* o, 
 {
     if (dtype == FA_DTYPE_FP16)
         return launch_decode_t<__half>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, stream, pg, win,
-                                       dw);
+                                       dw, nullptr, true);
     return launch_decode_t<__nv_bfloat16>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, stream, pg,
-                                          win, dw);
+                                          win, dw, nullptr, true);
 }
 
 // Keys of the longest list of visible tiles that a windowed decode may meet: Nk keys in a dense
@@ -985,6 +991,226 @@ fa_status_t noalloc_scratch(void** out)
     }
     *out = addr[dev];
     return FA_OK;
+}
+
+// ---------------------------------------------------------------------------
+// forward of a batch whose sequences share a prefix
+// ---------------------------------------------------------------------------
+struct PrefixArgs {
+    const void *q, *kp, *vp, *k, *v;
+    const int* lens;
+    void* o;
+    float* lse;
+    int B, Hq, Hkv, Nq, Np, Ns, d;
+    float scale;
+    int causal;
+};
+
+// Rows of several sequences fit a 128-row tile: the prefix in a pass of its own, which reads it
+// once for all of them, and a merge.  Where a sequence's rows fill half a tile or more, packing
+// saves nothing, and one launch reads the prefix and then the own keys.
+bool prefix_packs(const PrefixArgs& a) { return a.B > 1 && 2LL * (a.Hq / a.Hkv) * a.Nq <= 128; }
+
+// 4-D map over q as [B][Hkv][rows][d], box {64, rows, 1, pack}: a kv head's rows of `pack` sequences
+fa_status_t make_map_pack(CUtensorMap* m, const void* base, uint64_t d, uint64_t rows, uint64_t Hkv, uint64_t B,
+                          uint32_t pack, CUtensorMapDataType dt)
+{
+    EncodeTiledFn enc = get_encode();
+    if (!enc) {
+        set_error("cuTensorMapEncodeTiled is unavailable");
+        return FA_ERR_CUDA;
+    }
+    cuuint64_t dims[4] = {d, rows, Hkv, B};
+    cuuint64_t strides[3] = {d * 2, rows * d * 2, Hkv * rows * d * 2};
+    cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, pack};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = enc(m, dt, 4, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_error("cuTensorMapEncodeTiled (packed rows) failed (%d)", (int)r);
+        return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
+// Key shares of the packed prefix pass: the merge comes anyway, so the count is the one whose
+// rounds of work tiles over the SMs take the least time, a tile costing its key blocks and about
+// 2 block times, a share its fp32 partials (written and read at 13 MB per block time).
+int prefix_shares(long long units, int blocks, double part_bytes, int sms)
+{
+    int best = 1;
+    double best_cost = 0;
+    for (int s = 1; s <= 32 && s <= std::max(1, blocks / 2); ++s) {
+        const double cost = std::ceil((double)units * s / sms) * ((blocks + s - 1) / s + 2.0) + 2.0 * s * part_bytes / 13.0e6;
+        if (s == 1 || cost < 0.98 * best_cost) {
+            best = s;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
+// Tiled forward over prefix and own keys in one launch (np = 0: the own keys alone), final or,
+// with `part`, as partials ([B * Hkv][shares][rows]).  *shares: key shares (in / out with `part`).
+template <int D, typename T>
+fa_status_t launch_prefix_cat(const PrefixArgs& a, int np, float* part_o, float* part_lse, cudaStream_t stream)
+{
+    using C = fa::FwdCfg<D>;
+    CUtensorMap mq, mk, mv;
+    fa::FwdExtra<fa::kFwdCat> ex;
+    fa_status_t st;
+    FwdGeom g;
+    g.group_rows = 1;
+    g.n_bh = a.B * a.Hkv;
+    g.rows = a.Hq / a.Hkv * a.Nq;
+    g.n_pairs = (g.rows + 128 * C::kTiles - 1) / (128 * C::kTiles);
+    constexpr CUtensorMapDataType dt = tma_type<T>();
+    if ((st = make_map(&mq, a.q, a.d, g.rows, (uint64_t)g.n_bh, 128, dt)) != FA_OK) return st;
+    if ((st = make_map(&mk, a.kp, a.d, a.Np, (uint64_t)a.Hkv, 128, dt)) != FA_OK) return st;
+    if ((st = make_map(&mv, a.vp, a.d, a.Np, (uint64_t)a.Hkv, 128, dt)) != FA_OK) return st;
+    if ((st = make_map(&ex.k_own, a.k, a.d, a.Ns, (uint64_t)g.n_bh, 128, dt)) != FA_OK) return st;
+    if ((st = make_map(&ex.v_own, a.v, a.d, a.Ns, (uint64_t)g.n_bh, 128, dt)) != FA_OK) return st;
+    const int blocks = (np + 127) / 128 + (a.Ns + 127) / 128;
+    FwdSplit sp{1, 0};
+    if (!part_o)
+        sp = fwd_split_search(g, a.d, sm_count(), 4.0 * a.Hkv * ((double)a.Np + (double)a.B * a.Ns) * a.d,
+                              [&](int) { return blocks; });
+    auto kern = (part_o || sp.shares > 1) ? fa::fwd_kernel<D, true, T, false, true, fa::kFwdCat>
+                                          : fa::fwd_kernel<D, true, T, false, false, fa::kFwdCat>;
+    if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
+    fa::FwdParams p = fwd_params(g, a.o, a.lse, a.B, a.Hq, a.Hkv, a.Nq, a.Ns, a.d, a.scale * kLog2e, sp);
+    p.np = np;
+    p.seq_lens = a.lens;
+    p.causal = a.causal;
+    p.partial = part_o ? 1 : 0;
+    p.seq_rows = g.rows;
+    p.part_o = part_o;
+    p.part_lse = part_lse;
+    if ((st = fwd_tile_counter(&p.tile_ctr, &p.tile_tag)) != FA_OK)
+        return st;
+    return launch_fwd_tiles<T, fa::kFwdCat>(kern, C::kThreads, C::kSmemBytes, mq, mk, mv, p, stream, false, ex);
+}
+
+template <int D, typename T>
+fa_status_t launch_prefix_pack(const PrefixArgs& a, int shares, float* part_o, float* part_lse, cudaStream_t stream)
+{
+    using C = fa::FwdCfg<D>;
+    CUtensorMap mq, mk, mv;
+    fa_status_t st;
+    const int rows = a.Hq / a.Hkv * a.Nq, pack = 128 / rows;
+    FwdGeom g;
+    g.group_rows = 1;
+    g.n_bh = a.Hkv;
+    g.rows = (a.B + pack - 1) / pack * 128;
+    g.n_pairs = (g.rows + 128 * C::kTiles - 1) / (128 * C::kTiles);
+    constexpr CUtensorMapDataType dt = tma_type<T>();
+    if ((st = make_map_pack(&mq, a.q, a.d, rows, a.Hkv, a.B, pack, dt)) != FA_OK) return st;
+    if ((st = make_map(&mk, a.kp, a.d, a.Np, (uint64_t)a.Hkv, 128, dt)) != FA_OK) return st;
+    if ((st = make_map(&mv, a.vp, a.d, a.Np, (uint64_t)a.Hkv, 128, dt)) != FA_OK) return st;
+    auto kern = fa::fwd_kernel<D, true, T, false, true, fa::kFwdPack>;
+    if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
+    fa::FwdParams p = fwd_params(g, a.o, a.lse, a.B, a.Hq, a.Hkv, a.Nq, a.Ns, a.d, a.scale * kLog2e, {shares, 0});
+    p.np = a.Np;
+    p.seq_lens = a.lens;
+    p.causal = a.causal;
+    p.partial = 1;
+    p.seq_rows = rows;
+    p.pack = pack;
+    p.total_rows = (long long)a.B * a.Hq * a.Nq;
+    p.part_o = part_o;
+    p.part_lse = part_lse;
+    if ((st = fwd_tile_counter(&p.tile_ctr, &p.tile_tag)) != FA_OK)
+        return st;
+    return launch_fwd_tiles<T, fa::kFwdPack>(kern, C::kThreads, C::kSmemBytes, mq, mk, mv, p, stream);
+}
+
+struct PrefixPlan {
+    bool pack, decode;      // packed prefix pass; own keys by the split-KV decode
+    int shares;             // of the prefix pass
+    DecodePlan own;         // decode: its splits (else one share)
+    size_t a_lse, b_o, b_lse, total;   // workspace offsets (a_o at 0) and size; 0 without a merge
+};
+
+PrefixPlan prefix_plan(const PrefixArgs& a)
+{
+    PrefixPlan pl = {};
+    pl.pack = prefix_packs(a);
+    if (!pl.pack)
+        return pl;
+    const int rows = a.Hq / a.Hkv * a.Nq, pack = 128 / rows;
+    const size_t total_rows = (size_t)a.B * a.Hq * a.Nq;
+    const int kt = kernel_d(a.d) == 256 ? 1 : 2;
+    const int tiles = (a.B + pack - 1) / pack;
+    pl.shares = prefix_shares((long long)((tiles + kt - 1) / kt) * a.Hkv, (a.Np + 127) / 128, total_rows * a.d * 4.0,
+                              sm_count());
+    pl.decode = decode_shape(a.Hq, a.Hkv, a.Nq, a.d);
+    pl.own = decode_plan(a.B, a.Hq, a.Hkv, a.Nq, a.Ns, a.d, pl.decode ? 0 : 1);
+    pl.own.partial = true;
+    pl.a_lse = align256(total_rows * pl.shares * a.d * 4);
+    pl.b_o = pl.a_lse + align256(total_rows * pl.shares * 4);
+    const size_t b_o_bytes = pl.decode ? pl.own.o_bytes : total_rows * a.d * 4;
+    const size_t b_lse_bytes = pl.decode ? pl.own.lse_bytes : total_rows * 4;
+    pl.b_lse = pl.b_o + align256(b_o_bytes);
+    pl.total = pl.b_lse + align256(b_lse_bytes);
+    return pl;
+}
+
+template <int D, typename T>
+fa_status_t launch_prefix(const PrefixArgs& a, const PrefixPlan& pl, void* ws, cudaStream_t stream)
+{
+    if (!pl.pack)
+        return launch_prefix_cat<D, T>(a, a.Np, nullptr, nullptr, stream);
+    char* w = static_cast<char*>(ws);
+    float* a_o = reinterpret_cast<float*>(w);
+    float* a_lse = reinterpret_cast<float*>(w + pl.a_lse);
+    float* b_o = reinterpret_cast<float*>(w + pl.b_o);
+    float* b_lse = reinterpret_cast<float*>(w + pl.b_lse);
+    fa_status_t st = launch_prefix_pack<D, T>(a, pl.shares, a_o, a_lse, stream);
+    if (st != FA_OK)
+        return st;
+    const int rows = a.Hq / a.Hkv * a.Nq;
+    fa::PrefixMerge m = {};
+    m.nb = 1;
+    m.b_ld = a.d;
+    m.b_unit = 1.f;
+    if (pl.decode) {
+        if (a.lens)
+            st = launch_decode_t<T>(a.q, a.k, a.v, a.o, a.lse, a.B, a.Hq, a.Hkv, a.Nq, a.Ns, a.d, a.scale, a.causal, pl.own,
+                                    b_o, stream, nullptr, nullptr, nullptr, a.lens, false);
+        else
+            st = launch_decode_t<T>(a.q, a.k, a.v, a.o, a.lse, a.B, a.Hq, a.Hkv, a.Nq, a.Ns, a.d, a.scale, a.causal, pl.own,
+                                    b_o, stream, nullptr, nullptr, nullptr, nullptr, false);
+        m.nb = pl.own.splits;
+        m.b_ld = kDecodeWidth;
+        m.b_unit = kLog2e;
+    } else {
+        st = launch_prefix_cat<D, T>(a, 0, b_o, b_lse, stream);
+    }
+    if (st != FA_OK)
+        return st;
+    m.a_o = a_o;
+    m.a_lse = a_lse;
+    m.b_o = b_o;
+    m.b_lse = b_lse;
+    m.na = pl.shares;
+    m.seq_rows = rows;
+    m.d_io = a.d;
+    m.rows = (long long)a.B * a.Hq * a.Nq;
+    m.o = a.o;
+    m.lse = a.lse;
+    fa::prefix_merge_kernel<T><<<(unsigned)((m.rows + 3) / 4), 128, 0, stream>>>(m);
+    return check_launch("prefix_merge_kernel launch");
+}
+
+template <typename T>
+fa_status_t prefix_t(const PrefixArgs& a, const PrefixPlan& pl, void* ws, cudaStream_t s)
+{
+    if (kernel_d(a.d) == 256)
+        return launch_prefix<256, T>(a, pl, ws, s);
+    if (kernel_d(a.d) == 128)
+        return launch_prefix<128, T>(a, pl, ws, s);
+    return launch_prefix<64, T>(a, pl, ws, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -1858,6 +2084,61 @@ fa_status_t fa_fwd_paged_window(fa_dtype_t dtype, const void* q, const void* k_c
     const int w[2] = {window, sinks};
     return paged_entry((int)dtype, q, k_cache, v_cache, block_table, seq_lens, o, lse, B, Hq, Hkv, Nq, d, page_size,
                        num_pages, max_pages_per_seq, scale, 1, num_splits, workspace, workspace_bytes, stream, w);
+}
+
+static bool prefix_sizes_ok(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d)
+{
+    return B >= 1 && Hq >= 1 && Hkv >= 1 && Nq >= 1 && Np >= 1 && Ns >= 1 && Hq % Hkv == 0 && d >= 1 && d <= 256;
+}
+
+size_t fa_fwd_prefix_workspace_size(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d)
+{
+    if (!prefix_sizes_ok(B, Hq, Hkv, Nq, Np, Ns, d))
+        return 0;
+    return prefix_plan({nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, B, Hq, Hkv, Nq, Np, Ns, d, 1.f, 0})
+        .total;
+}
+
+fa_status_t fa_fwd_prefix(fa_dtype_t dtype, const void* q, const void* k_prefix, const void* v_prefix, const void* k,
+                          const void* v, const int* seq_lens, void* o, float* lse, int B, int Hq, int Hkv, int Nq,
+                          int Np, int Ns, int d, float scale, int causal, void* workspace, size_t workspace_bytes,
+                          void* stream)
+{
+    t_error.clear();
+    fa_status_t st;
+    if ((st = check_dtype((int)dtype)) || (st = check_ptr(q, "q")) || (st = check_ptr(k_prefix, "k_prefix")) ||
+        (st = check_ptr(v_prefix, "v_prefix")) || (st = check_ptr(k, "k")) || (st = check_ptr(v, "v")) ||
+        (st = check_ptr(o, "o")) || (st = check_float(lse, "lse", true)) || (st = check_float(seq_lens, "seq_lens", true)) ||
+        (st = check_shape(B, Hq, Hkv, Nq, Ns, d, scale, causal)) || (st = check_shape(1, Hq, Hkv, Nq, Np, d, scale, causal)))
+        return st;
+    if ((long long)Np + Ns > (1ll << 30) || (long long)(Hq / Hkv) * Nq > (1ll << 30)) {
+        set_error("problem too large for 32-bit positions");
+        return FA_ERR_UNSUPPORTED;
+    }
+    if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)) {
+        set_error("workspace is not 256-byte aligned");
+        return FA_ERR_INVALID_ARGUMENT;
+    }
+    const PrefixArgs a{q, k_prefix, v_prefix, k, v, seq_lens, o, lse, B, Hq, Hkv, Nq, Np, Ns, d, scale, causal};
+    const PrefixPlan pl = prefix_plan(a);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void* ws = workspace;
+    if (workspace && workspace_bytes < pl.total) {
+        set_error("workspace has %zu bytes, %zu needed", workspace_bytes, pl.total);
+        return FA_ERR_WORKSPACE;
+    }
+    if (!ws && pl.total > 0) {
+        cudaError_t e = scratch_alloc(&ws, pl.total, s);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "scratch allocation (prefix partials)");
+    }
+    st = dtype == FA_DTYPE_FP16 ? prefix_t<__half>(a, pl, ws, s) : prefix_t<__nv_bfloat16>(a, pl, ws, s);
+    if (ws && !workspace) {
+        cudaError_t e = cudaFreeAsync(ws, s);
+        if (e != cudaSuccess && st == FA_OK)
+            st = cuda_fail(e, "cudaFreeAsync");
+    }
+    return st;
 }
 
 fa_status_t fa_key_weights(fa_dtype_t dtype, const void* q, const void* k, const float* lse, const float* weights_in,

@@ -37,23 +37,42 @@ struct FwdParams {
     int pair_rows;      // query rows of a work unit: 256 (128 at d = 256)
     float* part_o;      // [n_bh, kv_split, rows, d_io] fp32: O_s = U_s / l_s of share s
     float* part_lse;    // [n_bh, kv_split, rows] fp32: m_s + log2(l_s), -inf where share s sees no key
-    // sliding window with sinks (fwd_kernel<..., WIN = true>, causal): key j is visible at query
+    // sliding window with sinks (kFwdWindow, causal): key j is visible at query
     // position x (in keys: i + Nk - Nq) iff j <= x and (j > x - window or j < sinks)
     int window;         // 1 .. Nk
     int sinks;          // 0 .. Nk
     int sink_full;      // whole 128-key blocks of sinks: sinks / 128
     int sink_rem;       // rows of the block after them that hold the other sinks, a multiple of 8
                         // (0: no such block; 128: it holds no window keys)
+    // shared prefix (kFwdPack, kFwdCat): sequence b's keys are the np prefix keys and its own
+    // first own_len(b) of Nk; with `causal` its Nq rows are the last Nq positions of the two
+    int np;             // prefix keys that the launch reads (0: own keys only)
+    const int* seq_lens;   // [B] own lengths, or nullptr (Nk each)
+    int causal;
+    int partial;        // partial results (part_o, part_lse) even of units that are not split
+    int seq_rows;       // rows of a (batch, kv head): G * Nq
+    int pack;           // kFwdPack: sequences in a 128-row tile: 128 / seq_rows
+    long long total_rows;   // B * Hq * Nq
 };
 
-// Extra TMA maps of a windowed forward: the block that holds both sinks and window keys is two
-// boxes, sink_rem rows of the first `sinks` keys (zero fill past them) and 128 - sink_rem rows
-// from the window's first key.
-template <bool WIN>
+// Key lists of the tiled forward.
+constexpr int kFwdPlain = 0;    // all keys of the tile head's kv head, causal or not
+constexpr int kFwdWindow = 1;   // sliding window with sinks
+constexpr int kFwdPack = 2;     // a shared prefix; a tile holds the rows of several sequences
+constexpr int kFwdCat = 3;      // a shared prefix, then the sequence's own keys
+
+// Extra TMA maps.  Window: the block that holds both sinks and window keys is two boxes, sink_rem
+// rows of the first `sinks` keys (zero fill past them) and 128 - sink_rem rows from the window's
+// first key.  Prefix and own keys: the maps of the own ones.
+template <int MODE>
 struct FwdExtra {};
 template <>
-struct FwdExtra<true> {
+struct FwdExtra<kFwdWindow> {
     CUtensorMap k_sink, v_sink, k_win, v_win;
+};
+template <>
+struct FwdExtra<kFwdCat> {
+    CUtensorMap k_own, v_own;
 };
 
 struct DecodeParams {

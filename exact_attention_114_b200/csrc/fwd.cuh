@@ -186,14 +186,21 @@ struct FwdTile {
     int share;     // key share (0 without a key split)
     int nshares;   // key shares of the tile's unit (1: the whole unit, written straight to o / lse)
     int wlo;       // sliding window: first window key of the tile (fwd_win_blocks)
+    int own;       // prefix and own keys: the sequence's own length
 };
+
+// Own length of sequence b.
+__device__ __forceinline__ int fwd_own_len(const FwdParams& p, int b)
+{
+    return p.seq_lens ? max(0, min(__ldg(p.seq_lens + b), p.Nk)) : p.Nk;
+}
 
 // The launch has at most one block per SM.  Block c starts with tile c; each
 // further tile is the next unclaimed one (the launch's tile counter), so like a
 // hardware block scheduler the blocks take the heavy causal tiles first and
 // whichever block is free takes the next.  With a key split (SPLIT) tile i is
 // share (i / (B*Hq)) % kv_split of its pair's key blocks.
-template <int kTiles, bool CAUSAL, bool SPLIT = false, bool WIN = false>
+template <int kTiles, bool CAUSAL, bool SPLIT = false, int MODE = kFwdPlain>
 __device__ __forceinline__ void fwd_tile(const FwdParams& p, int i, FwdTile& w)
 {
     const int n_bh = p.n_bh;
@@ -217,9 +224,29 @@ __device__ __forceinline__ void fwd_tile(const FwdParams& p, int i, FwdTile& w)
         w.kvh = b * p.Hkv + h / p.G;
     }
     w.q0 = pair * 128 * kTiles;
-    if constexpr (WIN) {
+    if constexpr (MODE == kFwdWindow) {
         int nb[2];
         fwd_win_blocks(w.q0, kTiles, p.rows, p.Nq, p.Nk, p.window, p.sinks, 128 * p.sink_full + p.sink_rem, w.wlo, nb);
+        w.nb0 = nb[0];
+        w.nb1 = nb[1];
+    } else if constexpr (MODE == kFwdPack) {
+        const int n = (p.np + 127) / 128;
+        w.nb0 = w.q0 < p.rows ? n : 0;
+        w.nb1 = (kTiles == 2 && w.q0 + 128 < p.rows) ? n : 0;
+    } else if constexpr (MODE == kFwdCat) {
+        w.own = fwd_own_len(p, w.bh / p.Hkv);
+        int nb[2] = {0, 0};
+        for (int t = 0; t < kTiles; ++t) {
+            const int qt = w.q0 + 128 * t;
+            if (qt >= p.rows)
+                continue;
+            int lo, hi;
+            fwd_positions(qt, p.rows, p.Nq, lo, hi);
+            // own keys that the tile's last position sees; none: it may see a part of the prefix
+            const int own = p.causal ? min(w.own, w.own - p.Nq + hi + 1) : w.own;
+            const int pre = p.np > 0 && p.causal ? min(p.np, p.np + w.own - p.Nq + hi + 1) : p.np;
+            nb[t] = own > 0 ? (p.np + 127) / 128 + (own + 127) / 128 : (max(pre, 0) + 127) / 128;
+        }
         w.nb0 = nb[0];
         w.nb1 = nb[1];
     } else {
@@ -254,14 +281,15 @@ __device__ __forceinline__ int fwd_take_tile(uint64_t* bar_tfull, uint64_t* bar_
 }
 
 // SPLIT: key split (kv_split shares per pair, partial results to part_o / part_lse);
-// without it the kernel carries none of the split's code.  WIN: sliding window with
-// sinks; only the tile's list of key blocks, their loads and their masks differ.
-template <int D, bool CAUSAL, typename T = __nv_bfloat16, bool F8 = false, bool SPLIT = false, bool WIN = false>
+// without it the kernel carries none of the split's code.  MODE: the tile's list of key
+// blocks (kFwdWindow, kFwdPack, kFwdCat); only the list, its loads and its masks differ, and
+// for kFwdPack the rows of a tile.
+template <int D, bool CAUSAL, typename T = __nv_bfloat16, bool F8 = false, bool SPLIT = false, int MODE = kFwdPlain>
 __global__ void __launch_bounds__(384, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdExtra<WIN> ex, FwdParams p)
+               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdExtra<MODE> ex, FwdParams p)
 {
-    static_assert(!WIN || (CAUSAL && !F8), "the window is causal, for 16-bit inputs");
+    static_assert(MODE == kFwdPlain || (CAUSAL && !F8), "other key lists: 16-bit inputs, one instance for both masks");
     using C = FwdCfg<D, F8>;
     griddep_launch_dependents();   // the merge of a key split may be scheduled
     extern __shared__ uint8_t smem_raw[];
@@ -348,7 +376,17 @@ __global__ void __launch_bounds__(384, 1)
             auto load_block = [&](uint8_t* dst, uint64_t* bar, int j, int kv) {
                 const CUtensorMap* tm = kv ? &tmV : &tmK;
                 int key = (w.kb0 + j) * 128;
-                if constexpr (WIN) {
+                if constexpr (MODE == kFwdCat) {
+                    const int npb = (p.np + 127) / 128;
+                    if (w.kb0 + j >= npb) {
+                        const CUtensorMap* own = kv ? &ex.v_own : &ex.k_own;
+                        for (int pn = 0; pn < C::kPanels; ++pn)
+                            tma_load_3d(dst + pn * C::kPanelBytes, own, bar, pn * C::kPanelElems, key - npb * 128, w.kvh);
+                        return;
+                    }
+                }
+                const int head = MODE == kFwdCat ? w.kvh % p.Hkv : w.kvh;   // the prefix has a head per kv head
+                if constexpr (MODE == kFwdWindow) {
                     const int jb = w.kb0 + j, rem = p.sink_rem;
                     if (jb >= p.sink_full) {
                         key = w.wlo + (jb - p.sink_full) * 128 - rem;
@@ -366,7 +404,7 @@ __global__ void __launch_bounds__(384, 1)
                     }
                 }
                 for (int pn = 0; pn < C::kPanels; ++pn)
-                    tma_load_3d(dst + pn * C::kPanelBytes, tm, bar, pn * C::kPanelElems, key, w.kvh);
+                    tma_load_3d(dst + pn * C::kPanelBytes, tm, bar, pn * C::kPanelElems, key, head);
             };
             // take the counter slot for this launch, or find it held by another one
             const unsigned owner = atomicCAS(p.tile_ctr + 2, 0u, p.tile_tag);
@@ -381,7 +419,7 @@ __global__ void __launch_bounds__(384, 1)
                 mbar_arrive(&bar_tfull[u & 1]);
                 if (tile >= n_tiles)
                     break;
-                fwd_tile<C::kTiles, CAUSAL, SPLIT, WIN>(p, tile, w);
+                fwd_tile<C::kTiles, CAUSAL, SPLIT, MODE>(p, tile, w);
                 for (int t = 0; t < 2 && ok; ++t) {
                     if ((t ? w.nb1 : w.nb0) == 0)
                         continue;
@@ -389,6 +427,19 @@ __global__ void __launch_bounds__(384, 1)
                     // the slot still holds the previous tile's Q until its last Q.K^T is done
                     if (nq > 0 && !(ok = mbar_wait(&bar_qfree[t], (uint32_t)((nq - 1) & 1), abort_flag)))
                         break;
+                    if constexpr (MODE == kFwdPack) {
+                        // `pack` sequences' rows of the kv head, one after another
+                        const int seq = (w.q0 / 128 + t) * p.pack;
+                        mbar_arrive_expect_tx(&bar_q[t], (uint32_t)(p.pack * p.seq_rows * 128 * C::kPanels));
+                        for (int pn = 0; pn < C::kPanels; ++pn)
+                            tma_load_4d(sQ + t * C::kTileBytes + pn * C::kPanelBytes, &tmQ, &bar_q[t],
+                                        pn * C::kPanelElems, 0, w.bh, seq);
+                        if (t)
+                            ++nq1;
+                        else
+                            ++nq0;
+                        continue;
+                    }
                     mbar_arrive_expect_tx(&bar_q[t], C::kTileBytes);
                     for (int pn = 0; pn < C::kPanels; ++pn)
                         tma_load_3d(sQ + t * C::kTileBytes + pn * C::kPanelBytes, &tmQ, &bar_q[t],
@@ -529,6 +580,22 @@ __global__ void __launch_bounds__(384, 1)
                 }
             };
 
+            // The own keys' last block: rows past the sequence's length hold whatever the batch's
+            // padding holds, which P = 0 would not keep out of P.V (0 * NaN): zero them
+            auto clean_v = [&](uint32_t slot_bytes, int j) {
+                if constexpr (MODE == kFwdCat) {
+                    const int first = w.own - (w.kb0 + j - (p.np + 127) / 128) * 128;   // first row to zero
+                    if (first >= 128 || w.kb0 + j < (p.np + 127) / 128)
+                        return;
+                    for (int pn = 0; pn < C::kPanels; ++pn)
+                        for (int i = first * 8 + lane; i < 1024; i += 32)
+                            *reinterpret_cast<uint4*>(sKV + slot_bytes + pn * C::kPanelBytes + i * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            };
+
             bool ok = true;
             // phase bits: 1 << t = parity of the Q loads of tile slot t waited for so far,
             // 4 << t = parity of the blocks of slot t in earlier tiles (bar_p phases)
@@ -542,7 +609,7 @@ __global__ void __launch_bounds__(384, 1)
                 const int tile = fwd_take_tile(bar_tfull, bar_tfree, tile_ring, u, lane, abort_flag, ok);
                 if (!ok || tile >= n_tiles)
                     break;
-                fwd_tile<C::kTiles, CAUSAL, SPLIT, WIN>(p, tile, w);
+                fwd_tile<C::kTiles, CAUSAL, SPLIT, MODE>(p, tile, w);
                 for (int t = 0; t < 2 && ok; ++t) {
                     if ((t ? w.nb1 : w.nb0) == 0)
                         continue;
@@ -579,6 +646,7 @@ __global__ void __launch_bounds__(384, 1)
                         const int b = j & 1;
                         if (!(ok = mbar_wait_w(&bar_full[1], (uint32_t)(vc & 1), abort_flag)))
                             break;
+                        clean_v((uint32_t)C::kTileBytes, j);
                         tc_fence_after();
                         const uint32_t pp = (uint32_t)((su[b] + (j >> 1)) & 1);
                         for (int hf = 0; hf < 2 && ok; ++hf) {
@@ -626,6 +694,7 @@ __global__ void __launch_bounds__(384, 1)
                     const int iv = k0 + 2 * j + 1, ik = k0 + 2 * j + 2;
                     if (!(ok = mbar_wait_w(&bar_full[iv % C::kStages], phase(iv), abort_flag)))
                         break;
+                    clean_v(slot_off(iv), j);
                     tc_fence_after();
                     bool k_ready = false;
                     for (int t = 0; t < 2 && ok; ++t) {
@@ -688,10 +757,27 @@ __global__ void __launch_bounds__(384, 1)
             const int tile = fwd_take_tile(bar_tfull, bar_tfree, tile_ring, u, lane, abort_flag, ok);
             if (!ok || tile >= n_tiles)
                 break;
-            fwd_tile<C::kTiles, CAUSAL, SPLIT, WIN>(p, tile, w);
+            fwd_tile<C::kTiles, CAUSAL, SPLIT, MODE>(p, tile, w);
             const int qi = w.q0 + 128 * t + r;   // row of the tile head
             const int nb = t ? w.nb1 : w.nb0;
             const int qlim = (p.group_rows ? qi % p.Nq : qi) + delta;   // last key its query position sees
+            // prefix and own keys: the last of each that the row sees, and (kFwdPack) the row's
+            // sequence, its place there, and its row among all
+            int pre_lim = 0, own_lim = 0;
+            long long flat = 0;
+            bool in_pack = true;
+            if constexpr (MODE == kFwdPack) {
+                const int sr = p.seq_rows, b = (qi / 128) * p.pack + r / sr;
+                in_pack = r / sr < p.pack && b < p.B;
+                flat = ((long long)b * p.Hkv + w.bh) * sr + r % sr;
+                pre_lim = p.np - 1;
+                if (p.causal && in_pack)
+                    pre_lim = min(pre_lim, p.np + fwd_own_len(p, b) - p.Nq + (r % sr) % p.Nq);
+            } else if constexpr (MODE == kFwdCat) {
+                const int x = w.own - p.Nq + qi % p.Nq;   // the row's position behind the prefix
+                pre_lim = p.causal ? min(p.np - 1, p.np + x) : p.np - 1;
+                own_lim = p.causal ? min(w.own - 1, x) : w.own - 1;
+            }
             float m_ref = -INFINITY, l = 0.f;
 
             for (int j = 0; j < nb; ++j) {
@@ -713,7 +799,18 @@ __global__ void __launch_bounds__(384, 1)
 
                 const int kb = (w.kb0 + j) * 128;
                 bool need_mask;
-                if constexpr (WIN) {
+                if constexpr (MODE == kFwdPack || MODE == kFwdCat) {
+                    const int npb = (p.np + 127) / 128;
+                    const bool pre = MODE == kFwdPack || w.kb0 + j < npb;
+                    const int last = pre ? pre_lim - kb : own_lim - (kb - npb * 128);   // last visible column
+                    need_mask = last < 127;
+                    if (need_mask) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c)
+                            if (c > last)
+                                s[c] = -INFINITY;
+                    }
+                } else if constexpr (MODE == kFwdWindow) {
                     // columns below `cut` are sinks, visible up to column shi; the others are
                     // window keys kw + c, visible from column wlo to whi
                     const int jb = w.kb0 + j;
@@ -733,7 +830,7 @@ __global__ void __launch_bounds__(384, 1)
                 } else {
                     need_mask = (kb + 128 > p.Nk) || (CAUSAL && kb + 127 > qlim);
                 }
-                if (!WIN && need_mask) {
+                if (MODE == kFwdPlain && need_mask) {
                     const int lim = CAUSAL ? min(p.Nk - 1, qlim) : p.Nk - 1;
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
@@ -849,8 +946,15 @@ __global__ void __launch_bounds__(384, 1)
                 break;
 
             // ---- epilogue: O = U / l (bf16), LSE = (m + log2 l) ln 2
-            const bool row_valid = (C::kTiles == 2 || t == 0) && qi < p.rows;   // one-tile blocks: warps 4-7 idle
+            const bool row_valid = (C::kTiles == 2 || t == 0) && qi < p.rows && in_pack;   // one-tile blocks: warps 4-7 idle
             const size_t row = (size_t)w.bh * (size_t)p.rows + (size_t)qi;   // the same flat row either way
+            const bool partial = SPLIT && (w.nshares > 1 || MODE == kFwdPack || (MODE == kFwdCat && p.partial));
+            // the row's place among the partials
+            auto part_row = [&]() -> size_t {
+                if constexpr (MODE == kFwdPack)
+                    return (size_t)w.share * (size_t)p.total_rows + (size_t)flat;
+                return ((size_t)w.bh * p.kv_split + w.share) * p.rows + qi;
+            };
             if (nb > 0) {
                 ok = mbar_wait(&bar_o[t], (uint32_t)(no & 1), abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
@@ -863,10 +967,10 @@ __global__ void __launch_bounds__(384, 1)
                 for (int c0 = 0; c0 < p.d_io; c0 += 32) {
                     uint32_t o[32];
                     tmem_ld32(tO + (uint32_t)c0, o);
-                    if (SPLIT && w.nshares > 1) {
+                    if (partial) {
                         // this share's normalised partial O_s in fp32
                         if (row_valid) {
-                            const size_t prow = ((size_t)w.bh * p.kv_split + w.share) * p.rows + qi;
+                            const size_t prow = part_row();
                             float4* dst = reinterpret_cast<float4*>(p.part_o + prow * p.d_io + c0);
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
@@ -890,16 +994,16 @@ __global__ void __launch_bounds__(384, 1)
                 // O(t) is read out: the next tile's first P.V may overwrite it once this
                 // warpgroup's P of that tile is signalled (after the fence in the P write)
                 tc_fence_before();
-                if (SPLIT && w.nshares > 1) {
+                if (partial) {
                     if (row_valid)
-                        p.part_lse[((size_t)w.bh * p.kv_split + w.share) * p.rows + qi] =
-                            (l > 0.f) ? m_ref + __log2f(l) : -INFINITY;
+                        p.part_lse[part_row()] = (l > 0.f) ? m_ref + __log2f(l) : -INFINITY;
                 } else if (row_valid && p.lse) {
                     p.lse[row] = (l > 0.f) ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
                 }
-            } else if (SPLIT && w.nshares > 1 && row_valid) {
+            } else if (partial) {
                 // no key of this share for any row of the tile: its partial carries no weight
-                p.part_lse[((size_t)w.bh * p.kv_split + w.share) * p.rows + qi] = -INFINITY;
+                if (row_valid)
+                    p.part_lse[part_row()] = -INFINITY;
             } else if (row_valid) {
                 // no visible key for any row of this tile
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + row * p.d_io);
@@ -1005,6 +1109,87 @@ __global__ void __launch_bounds__(128) fwd_combine_kernel(FwdParams p)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             if (k < n)
+                o[k] = Elt<T>::from_float(acc[k] * inv);
+    }
+    if (lane == 0 && p.lse)
+        p.lse[row] = (L > 0.f) ? (M + __log2f(L)) * kLn2 : -INFINITY;
+}
+
+// Merge of a shared prefix's partials with those of the own keys (one warp per query row), the
+// rescale-and-add of the online softmax as in fwd_combine_kernel: na shares of the prefix pass
+// ([na][rows]) and nb shares of the own keys' pass ([batch * kv heads][nb][seq_rows], from the tiled
+// forward or from the split-KV decode).
+struct PrefixMerge {
+    const float* a_o;
+    const float* a_lse;    // log2 units
+    const float* b_o;
+    const float* b_lse;    // times b_unit: log2 units
+    float b_unit;
+    int na, nb, b_ld;      // b_ld: floats per row of b_o
+    int seq_rows, d_io;
+    long long rows;
+    void* o;
+    float* lse;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(128) prefix_merge_kernel(PrefixMerge p)
+{
+    griddep_wait();
+    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= p.rows)
+        return;
+    const long long bh = row / p.seq_rows, r = row % p.seq_rows;
+    const int n = p.na + p.nb;
+    auto lse_of = [&](int s) {
+        return s < p.na ? p.a_lse[s * p.rows + row] : p.b_lse[(bh * p.nb + s - p.na) * p.seq_rows + r] * p.b_unit;
+    };
+    float M = -INFINITY;
+    for (int s = lane; s < n; s += 32)
+        M = fmaxf(M, lse_of(s));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    // lane l merges columns [c l, c l + c), c = d_io / 32
+    const int c = p.d_io / 32;
+    float acc[8], L = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        acc[k] = 0.f;
+    for (int s0 = 0; s0 < n && M != -INFINITY; s0 += 32) {
+        const float wl = s0 + lane < n ? ex2_approx(lse_of(s0 + lane) - M) : 0.f;
+#pragma unroll 4
+        for (int s = s0; s < min(n, s0 + 32); ++s) {
+            const float w = __shfl_sync(0xffffffffu, wl, s - s0);
+            if (w == 0.f)   // no key there (its O was never written) or a negligible share
+                continue;
+            L += w;
+            const float* o = (s < p.na ? p.a_o + (s * p.rows + row) * p.d_io
+                                       : p.b_o + ((bh * p.nb + s - p.na) * p.seq_rows + r) * p.b_ld) + c * lane;
+            if (c == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(o);
+                acc[0] = fmaf(w, v.x, acc[0]);
+                acc[1] = fmaf(w, v.y, acc[1]);
+                acc[2] = fmaf(w, v.z, acc[2]);
+                acc[3] = fmaf(w, v.w, acc[3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < c)
+                        acc[k] = fmaf(w, o[k], acc[k]);
+            }
+        }
+    }
+    const float inv = (L > 0.f) ? 1.f / L : 0.f;
+    T* o = static_cast<T*>(p.o) + row * p.d_io + c * lane;
+    if (c == 4) {
+        *reinterpret_cast<uint2*>(o) = make_uint2(Elt<T>::pack(acc[0] * inv, acc[1] * inv),
+                                                  Elt<T>::pack(acc[2] * inv, acc[3] * inv));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < c)
                 o[k] = Elt<T>::from_float(acc[k] * inv);
     }
     if (lane == 0 && p.lse)

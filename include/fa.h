@@ -364,6 +364,30 @@ fa_status_t fa_fwd_paged_window(fa_dtype_t dtype, const void* q, const void* k_c
                                 size_t workspace_bytes, void* stream);
 
 /*
+ * Forward of a batch whose sequences share a prefix (a common system prompt or
+ * document): the keys of sequence b are the Np prefix keys followed by its own
+ * first seq_lens[b] keys, under one softmax.
+ *   q, o [B,Hq,Nq,d]; k_prefix, v_prefix [Hkv,Np,d]; k, v [B,Hkv,Ns,d]; lse
+ *   [B,Hq,Nq] fp32 or NULL; seq_lens int32 [B] (device; clamped to 0 .. Ns) or
+ *   NULL (Ns each).  What k and v hold past a sequence's length does not matter.
+ *   causal = 1: the Nq rows of sequence b are the last Nq positions of its
+ *   Np + seq_lens[b] keys (bottom-right, as above; with fewer own keys than rows
+ *   the first rows lie inside the prefix).
+ * The result is that of fa_fwd_ex on the concatenated keys.  Where several
+ * sequences' rows (Nq * Hq / Hkv each) fit a tile of 128, the prefix is read and
+ * multiplied once for all of them, the own keys by the split-KV or the tiled
+ * kernel, and the partial results merged as blocks are (§04); otherwise one
+ * launch walks the prefix and then the own keys.
+ *   workspace: fa_fwd_prefix_workspace_size() bytes (0 where no partials are
+ *   merged), 256-byte aligned, or NULL (allocated stream-ordered).
+ */
+size_t fa_fwd_prefix_workspace_size(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d);
+fa_status_t fa_fwd_prefix(fa_dtype_t dtype, const void* q, const void* k_prefix, const void* v_prefix,
+                          const void* k, const void* v, const int* seq_lens, void* o, float* lse, int B, int Hq,
+                          int Hkv, int Nq, int Np, int Ns, int d, float scale, int causal, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
  * The weight that each key has received, for eviction from a KV cache.  Per
  * (batch, kv head) and key j, over all query rows i of the group's Hq / Hkv
  * heads:
