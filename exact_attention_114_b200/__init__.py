@@ -104,6 +104,8 @@ def lib() -> ctypes.CDLL:
             L.fa_fwd_window.restype = ip
             L.fa_bwd_window_workspace_size.argtypes = [ip] * 8
             L.fa_bwd_window_workspace_size.restype = sz
+            L.fa_bwd_window_query_split.argtypes = [ip] * 8 + [ctypes.POINTER(ip)]
+            L.fa_bwd_window_query_split.restype = ip
             L.fa_bwd_window.argtypes = [ip] + [vp] * 9 + [ip] * 6 + [fl, ip, ip, vp, sz, vp]
             L.fa_bwd_window.restype = ip
             L.fa_fwd_paged_window_workspace_size.argtypes = [ip] * 10
@@ -401,43 +403,84 @@ def fa_bwd(q, k, v, o, dout, lse, dq=None, dk=None, dv=None, *, causal=False, sc
 _NO_CONTEXT = contextlib.nullcontext()
 
 
-def _on_device(stream, q, **others):
-    """A context in which q's device (and `stream`, if given) is current, so that outputs are
-    allocated and kernels launched there; every other tensor must be on q's device."""
+def _on_device(stream, dev):
+    """A context in which `dev` (and `stream`, if given) is current, so that outputs are allocated and
+    kernels launched there."""
     import torch
-    if not q.is_cuda:
-        raise ValueError("q must be a contiguous CUDA tensor")
-    for name, t in others.items():
-        if t is not None and t.device != q.device:
-            raise ValueError(f"{name} is on {t.device}, q on {q.device}")
     if stream is not None:
-        if stream.device != q.device:
-            raise ValueError(f"stream is of {stream.device}, q on {q.device}")
+        if stream.device != dev:
+            raise ValueError(f"stream is of {stream.device}, the tensors on {dev}")
         return torch.cuda.stream(stream)
-    if q.device.index != torch.cuda.current_device():
-        return torch.cuda.device(q.device)
+    if dev.index != torch._C._cuda_getDevice():
+        return torch.cuda.device(dev)
     return _NO_CONTEXT
+
+
+def _raw_stream(dev):
+    """Handle of `dev`'s current stream (without the object that torch.cuda.current_stream() makes)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _leader(t, name):
+    """The device of a call's first tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t.device
+
+
+def _expect(t, name, dev, dtype, shape=None):
+    """Pointer of a contiguous tensor of `dtype` (and `shape`) on `dev`; None stays None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        _require(t, name, dtype, shape)
+    if t.device != dev:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}, it is on {t.device}")
+    return t.data_ptr()
+
+
+def _workspace(t, dev):
+    """(pointer, bytes) of a workspace, or (None, 0)."""
+    if t is None:
+        return None, 0
+    n = _ws_bytes(t)
+    if t.device != dev:
+        raise ValueError(f"workspace is on {t.device}, the tensors on {dev}")
+    return t.data_ptr(), n
 
 
 def _scale(scale, d):
     return 1.0 / math.sqrt(d) if scale is None else float(scale)
 
 
+def _qkv(q, k, v):
+    """Device, dtype code, sizes and pointers of q, k and v."""
+    B, Hq, Hkv, Nq, Nk, d = _dims(q, k)
+    code, dev, dt = _dtype_code(q), _leader(q, "q"), q.dtype
+    ptrs = (_expect(q, "q", dev, dt), _expect(k, "k", dev, dt), _expect(v, "v", dev, dt, k.shape))
+    return dev, code, (B, Hq, Hkv, Nq, Nk, d), ptrs
+
+
+def _new_lse(q):
+    import torch
+    return q.new_empty(q.shape[:3], dtype=torch.float32)
+
+
 def fa_fwd_window(q, k, v, window, sinks=0, o=None, lse=None, *, scale=None, stream=None, want_lse=True):
     """Forward with a sliding window and sinks (causal): each query sees the ``window`` newest keys
     up to its own and the first ``sinks`` keys.  bf16 or fp16; returns (o, lse)."""
     import torch
-    B, Hq, Hkv, Nq, Nk, d = _dims(q, k)
-    dt = _dtype_code(q)
-    _check_io(q, k, v, o, q.dtype)
-    _require_lse(lse, B, Hq, Nq)
-    with _on_device(stream, q, k=k, v=v, o=o, lse=lse):
+    dev, code, sizes, ptrs = _qkv(q, k, v)
+    _expect(o, "o", dev, q.dtype, q.shape)
+    _expect(lse, "lse", dev, torch.float32, q.shape[:3])
+    with _on_device(stream, dev):
         if o is None:
             o = torch.empty_like(q)
         if lse is None and want_lse:
-            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
-        _check(lib().fa_fwd_window(dt, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Nk, d,
-                                   _scale(scale, d), int(window), int(sinks), _stream(None)))
+            lse = _new_lse(q)
+        _check(lib().fa_fwd_window(code, *ptrs, o.data_ptr(), None if lse is None else lse.data_ptr(), *sizes,
+                                   _scale(scale, sizes[5]), int(window), int(sinks), _raw_stream(dev)))
     return o, lse
 
 
@@ -445,48 +488,32 @@ def fa_bwd_window_workspace_size(B, Hq, Hkv, Nq, Nk, d, window, sinks=0) -> int:
     return int(lib().fa_bwd_window_workspace_size(B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks)))
 
 
+def fa_bwd_window_query_split(B, Hq, Hkv, Nq, Nk, d, window, sinks=0):
+    """CTAs that share each unit of ``fa_bwd_window`` on the current device, given a full-size workspace:
+    (of a key block without sinks, of one with sinks); 0 for bad sizes."""
+    sink_split = ctypes.c_int(0)
+    split = lib().fa_bwd_window_query_split(B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks), ctypes.byref(sink_split))
+    return int(split), sink_split.value
+
+
 def fa_bwd_window(q, k, v, o, dout, lse, window, sinks=0, dq=None, dk=None, dv=None, *, scale=None,
                   workspace=None, stream=None):
     """Backward of ``fa_fwd_window``: returns (dq, dk, dv).  Allocates the gradients when not given."""
     import torch
-    B, Hq, Hkv, Nq, Nk, d = _dims(q, k)
-    dt = _dtype_code(q)
-    _check_io(q, k, v, o, q.dtype)
-    _require(dout, "dout", q.dtype, q.shape)
-    _require(lse, "lse", torch.float32, (B, Hq, Nq))
+    dev, code, sizes, ptrs = _qkv(q, k, v)
+    dt = q.dtype
+    ptrs += (_expect(o, "o", dev, dt, q.shape), _expect(dout, "dout", dev, dt, q.shape),
+             _expect(lse, "lse", dev, torch.float32, q.shape[:3]))
     for t, n, ref in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
-        if t is not None:
-            _require(t, n, q.dtype, ref.shape)
-    ws_bytes = _ws_bytes(workspace)
-    with _on_device(stream, q, k=k, v=v, o=o, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv, workspace=workspace):
+        _expect(t, n, dev, dt, ref.shape)
+    ws = _workspace(workspace, dev)
+    with _on_device(stream, dev):
         dq = torch.empty_like(q) if dq is None else dq
         dk = torch.empty_like(k) if dk is None else dk
         dv = torch.empty_like(v) if dv is None else dv
-        _check(lib().fa_bwd_window(dt, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
-                                   _ptr(dk), _ptr(dv), B, Hq, Hkv, Nq, Nk, d, _scale(scale, d), int(window),
-                                   int(sinks), _ptr(workspace), ws_bytes, _stream(None)))
+        _check(lib().fa_bwd_window(code, *ptrs, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *sizes,
+                                   _scale(scale, sizes[5]), int(window), int(sinks), *ws, _raw_stream(dev)))
     return dq, dk, dv
-
-
-def _paged_args(q, k_cache, v_cache, block_table, seq_lens, o, lse):
-    """Checked (dtype code, B, Hq, Hkv, Nq, d, page_size, num_pages, max_pages) of a paged call."""
-    import torch
-    B, Hq, Nq, d = q.shape
-    num_pages, page_size, Hkv, dk = k_cache.shape
-    if dk != d or tuple(v_cache.shape) != tuple(k_cache.shape):
-        raise ValueError("k_cache / v_cache shapes disagree with q")
-    dt = _dtype_code(q)
-    _require(q, "q", q.dtype)
-    _require(k_cache, "k_cache", q.dtype)
-    _require(v_cache, "v_cache", q.dtype)
-    _require(block_table, "block_table", torch.int32)
-    _require(seq_lens, "seq_lens", torch.int32, (B,))
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [B, max_pages_per_seq]")
-    if o is not None:
-        _require(o, "o", q.dtype, q.shape)
-    _require_lse(lse, B, Hq, Nq)
-    return dt, B, Hq, Hkv, Nq, d, page_size, num_pages, block_table.shape[1]
 
 
 def fa_fwd_paged_window_workspace_size(B, Hq, Hkv, Nq, page_size, max_pages_per_seq, d, window, sinks=0,
@@ -500,19 +527,26 @@ def fa_fwd_paged_window(q, k_cache, v_cache, block_table, seq_lens, window, sink
     """``fa_fwd_window`` for single tokens (or the last few) over a paged KV cache: arguments as
     ``fa_fwd_paged``, the window against each sequence's own length."""
     import torch
-    dt, B, Hq, Hkv, Nq, d, page_size, num_pages, max_pages = _paged_args(q, k_cache, v_cache, block_table,
-                                                                         seq_lens, o, lse)
-    ws_bytes = _ws_bytes(workspace)
-    with _on_device(stream, q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens, o=o,
-                    lse=lse, workspace=workspace):
+    B, Hq, Nq, d = q.shape
+    num_pages, page_size, Hkv, dk = k_cache.shape
+    code, dev, dt = _dtype_code(q), _leader(q, "q"), q.dtype
+    if dk != d or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache / v_cache shapes disagree with q")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages_per_seq]")
+    ptrs = (_expect(q, "q", dev, dt), _expect(k_cache, "k_cache", dev, dt), _expect(v_cache, "v_cache", dev, dt),
+            _expect(block_table, "block_table", dev, torch.int32), _expect(seq_lens, "seq_lens", dev, torch.int32, (B,)))
+    _expect(o, "o", dev, dt, q.shape)
+    _expect(lse, "lse", dev, torch.float32, q.shape[:3])
+    ws = _workspace(workspace, dev)
+    with _on_device(stream, dev):
         if o is None:
             o = torch.empty_like(q)
         if lse is None:
-            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
-        _check(lib().fa_fwd_paged_window(dt, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-                                         _ptr(seq_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, d, page_size,
-                                         num_pages, max_pages, _scale(scale, d), int(window), int(sinks),
-                                         int(num_splits), _ptr(workspace), ws_bytes, _stream(None)))
+            lse = _new_lse(q)
+        _check(lib().fa_fwd_paged_window(code, *ptrs, o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, d, page_size,
+                                         num_pages, block_table.shape[1], _scale(scale, d), int(window), int(sinks),
+                                         int(num_splits), *ws, _raw_stream(dev)))
     return o, lse
 
 
@@ -527,34 +561,23 @@ def fa_fwd_prefix(q, k_prefix, v_prefix, k, v, seq_lens=None, o=None, lse=None, 
     ``seq_lens[b]`` (int32 [B]; all without it).  Returns (o, lse), as ``fa_fwd`` on the
     concatenated keys would."""
     import torch
-    B, Hq, Hkv, Nq, Ns, d = _dims(q, k)
-    dt = _dtype_code(q)
-    _check_io(q, k, v, o, q.dtype)
+    dev, code, (B, Hq, Hkv, Nq, Ns, d), (qp, kp, vp) = _qkv(q, k, v)
+    dt = q.dtype
     if k_prefix.dim() != 3 or k_prefix.shape[0] != Hkv or k_prefix.shape[2] != d:
         raise ValueError(f"k_prefix has shape {tuple(k_prefix.shape)}, expected ({Hkv}, Np, {d})")
-    _require(k_prefix, "k_prefix", q.dtype)
-    _require(v_prefix, "v_prefix", q.dtype, k_prefix.shape)
-    if seq_lens is not None:
-        _require(seq_lens, "seq_lens", torch.int32, (B,))
-    _require_lse(lse, B, Hq, Nq)
-    ws_bytes = _ws_bytes(workspace)
-    with _on_device(stream, q, k_prefix=k_prefix, v_prefix=v_prefix, k=k, v=v, seq_lens=seq_lens, o=o, lse=lse,
-                    workspace=workspace):
+    ptrs = (qp, _expect(k_prefix, "k_prefix", dev, dt), _expect(v_prefix, "v_prefix", dev, dt, k_prefix.shape), kp, vp,
+            _expect(seq_lens, "seq_lens", dev, torch.int32, (B,)))
+    _expect(o, "o", dev, dt, q.shape)
+    _expect(lse, "lse", dev, torch.float32, q.shape[:3])
+    ws = _workspace(workspace, dev)
+    with _on_device(stream, dev):
         if o is None:
             o = torch.empty_like(q)
         if lse is None:
-            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
-        _check(lib().fa_fwd_prefix(dt, _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), _ptr(seq_lens),
-                                   _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, k_prefix.shape[1], Ns, d, _scale(scale, d),
-                                   int(bool(causal)), _ptr(workspace), ws_bytes, _stream(None)))
+            lse = _new_lse(q)
+        _check(lib().fa_fwd_prefix(code, *ptrs, o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, k_prefix.shape[1], Ns, d,
+                                   _scale(scale, d), int(bool(causal)), *ws, _raw_stream(dev)))
     return o, lse
-
-
-def _weights_io(weights, weights_out, k):
-    import torch
-    for t, n in ((weights, "weights"), (weights_out, "weights_out")):
-        if t is not None:
-            _require(t, n, torch.float32, k.shape[:3])
 
 
 def fa_key_weights(q, k, lse, weights=None, weights_out=None, *, causal=False, scale=None, stream=None):
@@ -562,17 +585,16 @@ def fa_key_weights(q, k, lse, weights=None, weights_out=None, *, causal=False, s
     if None): returns ``weights_out`` (a new tensor unless given; it may be ``weights`` itself).
     ``lse`` is that of the forward of the same q, k, scale and causal flag."""
     import torch
-    B, Hq, Hkv, Nq, Nk, d = _dims(q, k)
-    dt = _dtype_code(q)
-    _require(q, "q", q.dtype)
-    _require(k, "k", q.dtype)
-    _require(lse, "lse", torch.float32, (B, Hq, Nq))
-    _weights_io(weights, weights_out, k)
-    with _on_device(stream, q, k=k, lse=lse, weights=weights, weights_out=weights_out):
+    sizes = B, Hq, Hkv, Nq, Nk, d = _dims(q, k)
+    code, dev, f32 = _dtype_code(q), _leader(q, "q"), torch.float32
+    ptrs = (_expect(q, "q", dev, q.dtype), _expect(k, "k", dev, q.dtype), _expect(lse, "lse", dev, f32, (B, Hq, Nq)),
+            _expect(weights, "weights", dev, f32, k.shape[:3]))
+    _expect(weights_out, "weights_out", dev, f32, k.shape[:3])
+    with _on_device(stream, dev):
         if weights_out is None:
-            weights_out = torch.empty((B, Hkv, Nk), dtype=torch.float32, device=q.device)
-        _check(lib().fa_key_weights(dt, _ptr(q), _ptr(k), _ptr(lse), _ptr(weights), _ptr(weights_out), B, Hq, Hkv,
-                                    Nq, Nk, d, _scale(scale, d), int(bool(causal)), _stream(None)))
+            weights_out = k.new_empty(k.shape[:3], dtype=f32)
+        _check(lib().fa_key_weights(code, *ptrs, weights_out.data_ptr(), *sizes, _scale(scale, d), int(bool(causal)),
+                                    _raw_stream(dev)))
     return weights_out
 
 
@@ -582,21 +604,21 @@ def fa_fwd_weights(q, k, v, weights=None, weights_out=None, o=None, lse=None, *,
     ``weights`` [B, Hkv, Nk] fp32 (zeros if None) plus this call's, in a new tensor unless
     ``weights_out`` is given (it may be ``weights`` itself)."""
     import torch
-    B, Hq, Hkv, Nq, Nk, d = _dims(q, k)
-    dt = _dtype_code(q)
-    _check_io(q, k, v, o, q.dtype)
-    _require_lse(lse, B, Hq, Nq)
-    _weights_io(weights, weights_out, k)
-    with _on_device(stream, q, k=k, v=v, weights=weights, weights_out=weights_out, o=o, lse=lse):
+    dev, code, sizes, ptrs = _qkv(q, k, v)
+    f32 = torch.float32
+    _expect(o, "o", dev, q.dtype, q.shape)
+    _expect(lse, "lse", dev, f32, q.shape[:3])
+    w = _expect(weights, "weights", dev, f32, k.shape[:3])
+    _expect(weights_out, "weights_out", dev, f32, k.shape[:3])
+    with _on_device(stream, dev):
         if o is None:
             o = torch.empty_like(q)
         if lse is None:
-            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+            lse = _new_lse(q)
         if weights_out is None:
-            weights_out = torch.empty((B, Hkv, Nk), dtype=torch.float32, device=q.device)
-        _check(lib().fa_fwd_weights(dt, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(weights),
-                                    _ptr(weights_out), B, Hq, Hkv, Nq, Nk, d, _scale(scale, d), int(bool(causal)),
-                                    _stream(None)))
+            weights_out = k.new_empty(k.shape[:3], dtype=f32)
+        _check(lib().fa_fwd_weights(code, *ptrs, o.data_ptr(), lse.data_ptr(), w, weights_out.data_ptr(), *sizes,
+                                    _scale(scale, sizes[5]), int(bool(causal)), _raw_stream(dev)))
     return o, lse, weights_out
 
 
@@ -607,36 +629,33 @@ def fa_kv_evict(k, v, weights, keep, recent=0, seq_lens=None, k_out=None, v_out=
     None.  Returns (k_out, v_out, weights_out, index_out).  Of a sequence shorter than ``keep`` the rows
     behind its last key are left as they were; in outputs allocated here they are 0 (index -1)."""
     import torch
-    dt = _dtype_code(k)
-    if k.dim() != 4 or not k.is_cuda:
+    if k.dim() != 4:
         raise ValueError("k must be a contiguous CUDA tensor [B, Hkv, Nk, d]")
+    code, dev, dt, f32 = _dtype_code(k), _leader(k, "k"), k.dtype, torch.float32
     B, Hkv, Nk, d = k.shape
     keep, recent = int(keep), int(recent)
-    _require(k, "k", k.dtype)
-    _require(v, "v", k.dtype, k.shape)
-    _require(weights, "weights", torch.float32, (B, Hkv, Nk))
-    if seq_lens is not None:
-        _require(seq_lens, "seq_lens", torch.int32, (B,))
     if not 0 <= recent <= keep or keep < 1:
         raise ValueError(f"keep={keep} must be >= 1 and recent={recent} in [0, keep]")
-    for t, n, dtype, shape in ((k_out, "k_out", k.dtype, (B, Hkv, keep, d)), (v_out, "v_out", k.dtype, (B, Hkv, keep, d)),
-                               (weights_out, "weights_out", torch.float32, (B, Hkv, keep)),
-                               (index_out, "index_out", torch.int32, (B, Hkv, keep))):
-        if t is not None:
-            _require(t, n, dtype, shape)
-    with _on_device(stream, k, v=v, weights=weights, seq_lens=seq_lens, k_out=k_out, v_out=v_out,
-                    weights_out=weights_out, index_out=index_out):
-        def new(shape, dtype, fill):
+    ptrs = (_expect(k, "k", dev, dt), _expect(v, "v", dev, dt, k.shape), _expect(weights, "weights", dev, f32, k.shape[:3]),
+            _expect(seq_lens, "seq_lens", dev, torch.int32, (B,)))
+    _expect(k_out, "k_out", dev, dt, (B, Hkv, keep, d))
+    _expect(v_out, "v_out", dev, dt, (B, Hkv, keep, d))
+    _expect(weights_out, "weights_out", dev, f32, (B, Hkv, keep))
+    _expect(index_out, "index_out", dev, torch.int32, (B, Hkv, keep))
+    with _on_device(stream, dev):
+        def new(t, shape, dtype, fill):
+            if t is not None:
+                return t
             if seq_lens is None and keep <= Nk:   # every row is written
-                return torch.empty(shape, dtype=dtype, device=k.device)
-            return torch.full(shape, fill, dtype=dtype, device=k.device)
+                return k.new_empty(shape, dtype=dtype)
+            return k.new_full(shape, fill, dtype=dtype)
 
-        k_out = new((B, Hkv, keep, d), k.dtype, 0) if k_out is None else k_out
-        v_out = new((B, Hkv, keep, d), k.dtype, 0) if v_out is None else v_out
-        weights_out = new((B, Hkv, keep), torch.float32, 0) if weights_out is None else weights_out
-        index_out = new((B, Hkv, keep), torch.int32, -1) if index_out is None else index_out
-        _check(lib().fa_kv_evict(dt, _ptr(k), _ptr(v), _ptr(weights), _ptr(seq_lens), _ptr(k_out), _ptr(v_out),
-                                 _ptr(weights_out), _ptr(index_out), B, Hkv, Nk, d, keep, recent, _stream(None)))
+        k_out = new(k_out, (B, Hkv, keep, d), dt, 0)
+        v_out = new(v_out, (B, Hkv, keep, d), dt, 0)
+        weights_out = new(weights_out, (B, Hkv, keep), f32, 0)
+        index_out = new(index_out, (B, Hkv, keep), torch.int32, -1)
+        _check(lib().fa_kv_evict(code, *ptrs, k_out.data_ptr(), v_out.data_ptr(), weights_out.data_ptr(),
+                                 index_out.data_ptr(), B, Hkv, Nk, d, keep, recent, _raw_stream(dev)))
     return k_out, v_out, weights_out, index_out
 
 

@@ -280,6 +280,10 @@ __device__ __forceinline__ void bwd_q_range(const BwdParams& p, int kb, int& qb0
     nqb = max(0, nqb_all - qb0);
 }
 
+// Partial slots of a unit that nsp CTAs share: none for one, one for two (the last CTA adds the
+// other's to its own sums), one per CTA for more.
+__host__ __device__ constexpr int bwd_part_slots(int nsp) { return nsp == 1 ? 0 : nsp == 2 ? 1 : nsp; }
+
 // The same under a sliding window with sinks: the last query that sees a key j >= sinks is at
 // position j + window - 1; a block that holds sinks is seen by every later query.
 __host__ __device__ __forceinline__ void bwd_win_q_range(int kb, int Nq, int Nk, int window, int sinks, int& qb0,
@@ -848,8 +852,7 @@ __global__ void __launch_bounds__(384, 1)
                 cta_e -= n_sink;
                 unit_e = part_units + cta_e / nsp;
                 // the sinks' units come first, with slots of their own count
-                const int slots_s = p.sink_split == 2 ? 1 : p.sink_split, slots_q = nsp == 2 ? 1 : nsp;
-                slot_e = (size_t)part_units * slots_s - (size_t)part_units * slots_q;
+                slot_e = (size_t)part_units * bwd_part_slots(p.sink_split) - (size_t)part_units * bwd_part_slots(nsp);
             }
         }
         int* n_written = SPLIT ? p.split_cnt + p.n_split_units + unit_e : nullptr;

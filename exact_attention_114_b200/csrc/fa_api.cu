@@ -1323,7 +1323,7 @@ BwdWinPlan bwd_win_plan(const BwdPlan& base, int B, int Hq, int Hkv, int Nq, int
     static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
     const double slot_bytes = 2.0 * std::min(kd, 128) * 128 * 4;
     const double sink_units = pl.sink_blocks * per_kb, other_units = (n_kb - pl.sink_blocks) * per_kb;
-    auto slots = [](int s) { return s == 1 ? 0 : s == 2 ? 1 : s; };
+    auto slots = [](int s) { return fa::bwd_part_slots(s); };
     auto fixed = [](int s) { return 8.5 + (s > 1 ? 0.8 * (s - 1) : 0.0); };
     pl.sink_split = pl.q_split = 1;
     double best = 0;
@@ -2052,6 +2052,17 @@ size_t fa_bwd_window_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int 
         return 0;
     const Window w{std::min(window, Nk), std::min(sinks, Nk)};
     return bwd_win_plan(bwd_plan(B, Hq, Hkv, Nq, Nk, d), B, Hq, Hkv, Nq, Nk, d, w, sm_count()).total_split;
+}
+
+int fa_bwd_window_query_split(int B, int Hq, int Hkv, int Nq, int Nk, int d, int window, int sinks, int* sink_split)
+{
+    if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Nk < 1 || Hq % Hkv != 0 || d < 1 || d > 256 || window < 1 || sinks < 0)
+        return 0;
+    const Window w{std::min(window, Nk), std::min(sinks, Nk)};
+    const BwdWinPlan pl = bwd_win_plan(bwd_plan(B, Hq, Hkv, Nq, Nk, d), B, Hq, Hkv, Nq, Nk, d, w, sm_count());
+    if (sink_split)
+        *sink_split = pl.sink_split;
+    return pl.q_split;
 }
 
 fa_status_t fa_bwd_window(fa_dtype_t dtype, const void* q, const void* k, const void* v, const void* o,

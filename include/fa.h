@@ -344,6 +344,10 @@ fa_status_t fa_fwd_window(fa_dtype_t dtype, const void* q, const void* k, const 
  * least the size without the partials runs unshared.
  */
 size_t fa_bwd_window_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int d, int window, int sinks);
+/* CTAs that share each unit of a key block without sinks, and (*sink_split, unless NULL) of
+ * a block with sinks, given a full-size workspace or none; 0 for sizes it would refuse. */
+int fa_bwd_window_query_split(int B, int Hq, int Hkv, int Nq, int Nk, int d, int window, int sinks,
+                              int* sink_split);
 fa_status_t fa_bwd_window(fa_dtype_t dtype, const void* q, const void* k, const void* v, const void* o,
                           const void* dout, const float* lse, void* dq, void* dk, void* dv, int B, int Hq,
                           int Hkv, int Nq, int Nk, int d, float scale, int window, int sinks, void* workspace,

@@ -159,6 +159,32 @@ def test_backward_repeats_and_workspaces(shared):
         assert torch.equal(again[1], first[1]) and torch.equal(again[2], first[2])
 
 
+# shapes whose plans differ: the units of the sinks' blocks shared, the others, both, neither
+SPLITS = [((1, 8, 1, 1500, 1500, 64, 1400, 4), True, True), ((1, 2, 1, 4000, 4000, 64, 130, 4), False, True),
+          ((1, 32, 8, 8192, 8192, 64, 4096, 4), True, False), ((2, 8, 8, 1000, 1000, 64, 200, 1), False, False),
+          ((1, 8, 1, 2048, 2048, 64, 512, 0), True, False)]
+
+
+@pytest.mark.parametrize("case", SPLITS, ids=str)
+def test_backward_stays_inside_its_workspace(case):
+    shape, others, sinks_too = case
+    split, sink_split = fa.fa_bwd_window_query_split(*shape)
+    assert (split > 1, sink_split > 1) == (others, sinks_too)
+    B, Hq, Hkv, Nq, Nk, d, window, sinks = shape
+    q, k, v, dout = make(B, Hq, Hkv, Nq, Nk, d, BF16, 550)
+    o, lse = fa.fa_fwd_window(q, k, v, window, sinks)
+    n, guard = fa.fa_bwd_window_workspace_size(*shape), 1 << 21
+    buf = torch.full((n + 2 * guard,), 0x5A, dtype=torch.uint8, device="cuda")
+    got = fa.fa_bwd_window(q, k, v, o, dout, lse, window, sinks, workspace=buf[guard:guard + n])
+    torch.cuda.synchronize()
+    fa.fa_check_device_status()
+    assert (buf[:guard] == 0x5A).all() and (buf[guard + n:] == 0x5A).all()
+    Hn, G = min(Hkv, 2), Hq // Hkv   # the last kv heads against fp64
+    r = ref_of(q[:, -Hn * G:], k[:, -Hn:], v[:, -Hn:], window, sinks, dout[:, -Hn * G:])
+    for x, ref, tol in zip(got, (r.dq, r.dk, r.dv), (r.dq_tol, r.dk_tol, r.dv_tol)):
+        close(x[:, -ref.shape[1] * x.shape[1] // Hkv:].reshape(ref.shape), ref, tol, "gradient")
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 @pytest.mark.parametrize("Nq,Hq", [(1, 4), (3, 4), (200, 2), (40, 8)])
 def test_unseen_keys_may_hold_anything(Nq, Hq, bad):

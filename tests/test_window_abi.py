@@ -40,6 +40,26 @@ def test_backward_refuses():
     assert fa.fa_bwd_window_workspace_size(1, 2, 1, 300, 300, 64, 10, 4) >= 2 * 2 * 320 * 4 + 2 * 320 * 64 * 4
 
 
+@pytest.mark.parametrize("shape", [(1, 32, 8, 8192, 8192, 128, 4096, 4), (1, 32, 8, 8192, 8192, 128, 1024, 4),
+                                   (1, 8, 1, 1500, 1500, 64, 1400, 4), (1, 2, 1, 2500, 2500, 256, 70, 200),
+                                   (2, 8, 8, 1000, 1000, 64, 200, 1), (1, 8, 1, 2048, 2048, 128, 512, 0)], ids=str)
+def test_workspace_holds_every_partial(shape):
+    """The workspace's partials are the slots that the launch's units use: of a unit shared by n CTAs none for
+    n = 1, one for n = 2, n for more, the sinks' units and the others each with their own n."""
+    B, Hq, Hkv, Nq, Nk, d, window, sinks = shape
+    up = lambda x: (x + 255) // 256 * 256  # noqa: E731
+    rows, kd = B * Hq * (-(-Nq // 64) * 64), 64 if d <= 64 else 128 if d <= 128 else 256
+    least = 2 * up(rows * 4) + up(rows * kd * 4)
+    split, sink_split = fa.fa_bwd_window_query_split(*shape)
+    per_block = B * Hkv * (2 if kd == 256 else 1)
+    n_kb, sink_kb = -(-Nk // 128), -(-min(sinks, Nk) // 128)
+    slots = lambda n: 0 if n == 1 else 1 if n == 2 else n  # noqa: E731
+    n = per_block * (sink_kb * slots(sink_split) + (n_kb - sink_kb) * slots(split))
+    want = least if n == 0 else least + up(n * 2 * min(kd, 128) * 128 * 4) + up(per_block * n_kb * 8)
+    assert fa.fa_bwd_window_workspace_size(*shape) == want
+    assert fa.fa_bwd_window_query_split(1, 3, 2, 8, 8, 64, 1) == (0, 0)
+
+
 def test_paged_refuses():
     def call(window=10, sinks=0, page=64, Nq=1, d=128, table=FAKE, ws=None, n=0, splits=0):
         return fa.lib().fa_fwd_paged_window(0, FAKE, FAKE, FAKE, table, FAKE, FAKE, None, 2, 8, 2, Nq, d, page, 100,
