@@ -117,6 +117,12 @@ __device__ __forceinline__ int fwd_blocks_for_tile(int qt, int rows, int Nq, int
     return min(nkb, last_key / 128 + 1);
 }
 
+// The low n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n)
+{
+    return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+
 // Positions of the query rows [qt, qt + 128) of a tile head: smallest and largest (row r at
 // position r % Nq).  Only for qt < rows.
 __host__ __device__ __forceinline__ void fwd_positions(int qt, int rows, int Nq, int& lo, int& hi)
@@ -761,6 +767,13 @@ __global__ void __launch_bounds__(384, 1)
             const int qi = w.q0 + 128 * t + r;   // row of the tile head
             const int nb = t ? w.nb1 : w.nb0;
             const int qlim = (p.group_rows ? qi % p.Nq : qi) + delta;   // last key its query position sees
+            // window: the row's first window key; the last of the warp's firsts, the first of its lasts
+            int win_lo = 0, warp_lo = 0, warp_hi = 0;
+            if constexpr (MODE == kFwdWindow) {
+                win_lo = max(p.sinks, qlim - p.window + 1);
+                warp_lo = __reduce_max_sync(0xffffffffu, win_lo);
+                warp_hi = __reduce_min_sync(0xffffffffu, qlim);
+            }
             // prefix and own keys: the last of each that the row sees, and (kFwdPack) the row's
             // sequence, its place there, and its row among all
             int pre_lim = 0, own_lim = 0;
@@ -811,21 +824,26 @@ __global__ void __launch_bounds__(384, 1)
                                 s[c] = -INFINITY;
                     }
                 } else if constexpr (MODE == kFwdWindow) {
-                    // columns below `cut` are sinks, visible up to column shi; the others are
-                    // window keys kw + c, visible from column wlo to whi
                     const int jb = w.kb0 + j;
-                    const int cut = jb < p.sink_full ? 128 : jb == p.sink_full ? p.sink_rem : 0;
-                    const int shi = min(p.sinks - 1, qlim) - kb;
-                    const int kw = w.wlo + (jb - p.sink_full) * 128 - p.sink_rem;
-                    int wlo = max(p.sinks, qlim - p.window + 1) - kw, whi = qlim - kw;
-                    if (whi < wlo)
-                        wlo = whi = 128;
-                    need_mask = (cut > 0 && shi < cut - 1) || (cut < 128 && (wlo > cut || whi < 127));
+                    const int kw = w.wlo + (jb - p.sink_full) * 128 - p.sink_rem;   // key of column 0 among the window's
+                    const bool all_sinks = jb < p.sink_full, some = jb == p.sink_full && p.sink_rem > 0;
+                    // all 128 keys visible to all rows of the warp
+                    need_mask = all_sinks ? kb + 127 > warp_hi : some || kw < warp_lo || kw + 127 > warp_hi;
                     if (need_mask) {
+                        // the visible columns as bits, a word per 32: n_sink sinks at the start (of
+                        // `cut` places), window keys from wlo to whi (none below `cut`)
+                        const int cut = all_sinks ? 128 : some ? p.sink_rem : 0;
+                        const int n_sink = min(min(p.sinks - 1, qlim) + 1 - kb, cut);
+                        const int wlo = win_lo - kw, whi = qlim - kw;
 #pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            if (c < cut ? c > shi : (unsigned)(c - wlo) > (unsigned)(whi - wlo))
-                                s[c] = -INFINITY;
+                        for (int g = 0; g < 4; ++g) {
+                            const uint32_t seen = bits_below(n_sink - 32 * g) |
+                                                  (bits_below(whi + 1 - 32 * g) & ~bits_below(wlo - 32 * g));
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!((seen >> c) & 1u))
+                                    s[32 * g + c] = -INFINITY;
+                        }
                     }
                 } else {
                     need_mask = (kb + 128 > p.Nk) || (CAUSAL && kb + 127 > qlim);
@@ -879,7 +897,7 @@ __global__ void __launch_bounds__(384, 1)
                 // core at d = 128, so there (kPoly) in blocks without masked scores
                 // one pair in four goes to the FMA-pipe exp2 instead (masked -inf
                 // scores always take ex2.approx, which returns exactly 0 for them).
-                const bool soft = C::kPoly && !__any_sync(0xffffffffu, need_mask);
+                const bool soft = C::kPoly && (MODE == kFwdWindow ? !need_mask : !__any_sync(0xffffffffu, need_mask));
                 auto half_block_f8 = [&](int hf, auto use_poly) {
                     uint32_t pk[16];
 #pragma unroll
