@@ -783,9 +783,20 @@ __global__ void __launch_bounds__(384, 1)
             uint32_t pp[32], dd[32];
             const float2 sl22 = make_float2(sl2, sl2);
             // rows >= min_row see the key; whole 64-row block visible in most steps
-            // (and, under a window, rows <= max_row)
-            const int max_row = !WIN || key < p.sinks ? INT_MAX : min_row + p.window - 1;
-            const bool all_vis = key_ok && (q_first >= min_row) && (!WIN || q_first + 63 <= max_row);
+            bool all_vis = key_ok && (q_first >= min_row);
+            // under a window, also rows <= max_row: the step's visible rows as bits, a word per 32,
+            // looked at only where a key of the warp does not see all 64
+            uint32_t seen[2] = {0u, 0u};
+            if constexpr (WIN) {
+                const int max_row = key < p.sinks ? INT_MAX : min_row + p.window - 1;
+                all_vis = __all_sync(0xffffffffu, all_vis && q_first + 63 <= max_row);
+                if (!all_vis && key_ok) {
+                    const int lo = min_row - q_first, n = min(max_row - q_first, 63) + 1;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+                        seen[g] = bits_below(n - 32 * g) & ~bits_below(lo - 32 * g);
+                }
+            }
 #pragma unroll
             for (int c4 = 0; c4 < 16; ++c4) {
                 const float4 nl4 = nlse4[c4], nd4 = ndlt4[c4];
@@ -798,8 +809,13 @@ __global__ void __launch_bounds__(384, 1)
                         ffma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl22, nl);
                     float2 pv = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                     if (!all_vis) {
-                        pv.x = (key_ok && q_first + c >= min_row && (!WIN || q_first + c <= max_row)) ? pv.x : 0.f;
-                        pv.y = (key_ok && q_first + c + 1 >= min_row && (!WIN || q_first + c + 1 <= max_row)) ? pv.y : 0.f;
+                        if constexpr (WIN) {
+                            pv.x = ((seen[c >> 5] >> (c & 31)) & 1u) ? pv.x : 0.f;
+                            pv.y = ((seen[c >> 5] >> ((c & 31) + 1)) & 1u) ? pv.y : 0.f;
+                        } else {
+                            pv.x = (key_ok && q_first + c >= min_row) ? pv.x : 0.f;
+                            pv.y = (key_ok && q_first + c + 1 >= min_row) ? pv.y : 0.f;
+                        }
                     }
                     // dS = P * (dP - D)
                     const float2 dd2 = fadd2(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), nd);

@@ -1328,7 +1328,9 @@ BwdWinPlan bwd_win_plan(const BwdPlan& base, int B, int Hq, int Hkv, int Nq, int
     pl.sink_split = pl.q_split = 1;
     double best = 0;
     for (int ss : kSplits) {
-        if (ss > 1 && (longest[0] < 16.0 * ss || pl.sink_blocks == 0))
+        // (a sinks' CTA keeps at least 4 steps: where the others' units are short, a sinks' unit of 16
+        // steps is the longest CTA of the launch)
+        if (ss > 1 && (longest[0] < 4.0 * ss || pl.sink_blocks == 0))
             break;
         for (int qs : kSplits) {
             if (qs > 8 || (qs > 1 && longest[1] < 16.0 * qs))

@@ -117,12 +117,6 @@ __device__ __forceinline__ int fwd_blocks_for_tile(int qt, int rows, int Nq, int
     return min(nkb, last_key / 128 + 1);
 }
 
-// The low n bits (none for n <= 0, all for n >= 32).
-__device__ __forceinline__ uint32_t bits_below(int n)
-{
-    return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
-}
-
 // Positions of the query rows [qt, qt + 128) of a tile head: smallest and largest (row r at
 // position r % Nq).  Only for qt < rows.
 __host__ __device__ __forceinline__ void fwd_positions(int qt, int rows, int Nq, int& lo, int& hi)

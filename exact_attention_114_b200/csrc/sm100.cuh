@@ -648,6 +648,12 @@ struct Elt<__half> {
     __device__ static __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
 };
 
+// The low n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n)
+{
+    return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+
 __device__ __forceinline__ int warp_id() { return threadIdx.x >> 5; }
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 31; }
 
