@@ -108,9 +108,9 @@ def lib() -> ctypes.CDLL:
             L.fa_bwd_window_query_split.restype = ip
             L.fa_bwd_window.argtypes = [ip] + [vp] * 9 + [ip] * 6 + [fl, ip, ip, vp, sz, vp]
             L.fa_bwd_window.restype = ip
-            L.fa_fwd_paged_window_workspace_size.argtypes = [ip] * 10
+            L.fa_fwd_paged_window_workspace_size.argtypes = [ip] * 9
             L.fa_fwd_paged_window_workspace_size.restype = sz
-            L.fa_fwd_paged_window.argtypes = [ip] + [vp] * 7 + [ip] * 8 + [fl, ip, ip, ip, vp, sz, vp]
+            L.fa_fwd_paged_window.argtypes = [ip] + [vp] * 7 + [ip] * 8 + [fl, ip, ip, vp, sz, vp]
             L.fa_fwd_paged_window.restype = ip
             L.fa_key_weights.argtypes = [ip] + [vp] * 5 + [ip] * 6 + [fl, ip, vp]
             L.fa_key_weights.restype = ip
@@ -516,14 +516,13 @@ def fa_bwd_window(q, k, v, o, dout, lse, window, sinks=0, dq=None, dk=None, dv=N
     return dq, dk, dv
 
 
-def fa_fwd_paged_window_workspace_size(B, Hq, Hkv, Nq, page_size, max_pages_per_seq, d, window, sinks=0,
-                                       num_splits=0) -> int:
+def fa_fwd_paged_window_workspace_size(B, Hq, Hkv, Nq, page_size, max_pages_per_seq, d, window, sinks=0) -> int:
     return int(lib().fa_fwd_paged_window_workspace_size(B, Hq, Hkv, Nq, page_size, max_pages_per_seq, d,
-                                                        int(window), int(sinks), num_splits))
+                                                        int(window), int(sinks)))
 
 
 def fa_fwd_paged_window(q, k_cache, v_cache, block_table, seq_lens, window, sinks=0, o=None, lse=None, *,
-                        scale=None, num_splits=0, workspace=None, stream=None):
+                        scale=None, workspace=None, stream=None):
     """``fa_fwd_window`` for single tokens (or the last few) over a paged KV cache: arguments as
     ``fa_fwd_paged``, the window against each sequence's own length."""
     import torch
@@ -546,7 +545,7 @@ def fa_fwd_paged_window(q, k_cache, v_cache, block_table, seq_lens, window, sink
             lse = _new_lse(q)
         _check(lib().fa_fwd_paged_window(code, *ptrs, o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, d, page_size,
                                          num_pages, block_table.shape[1], _scale(scale, d), int(window), int(sinks),
-                                         int(num_splits), *ws, _raw_stream(dev)))
+                                         *ws, _raw_stream(dev)))
     return o, lse
 
 

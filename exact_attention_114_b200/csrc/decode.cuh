@@ -82,30 +82,9 @@ __device__ __forceinline__ uint32_t dec_tile_off(int key, int chunk)
     return (uint32_t)(panel * DecCfg::kPanelBytes + key * 128 + ((c ^ (key & 7)) << 4));
 }
 
-// Tiles of the visible keys under a sliding window with sinks, for Nq rows at the last positions
-// of Nk keys: ceil(sinks / 64) tiles from key 0, then tiles from win_base on (64-aligned in a
-// paged cache, so that none straddles a page).  Returns their number; win_lo is the first row's
-// first window key.
-__host__ __device__ __forceinline__ int dec_win_tiles(int Nk, int Nq, int window, int sinks, bool paged, int& win_lo,
-                                                      int& sink_tiles, int& win_base)
-{
-    const int s = sinks < Nk ? sinks : Nk;
-    const int first = Nk - Nq - window + 1;
-    win_lo = first > 0 ? first : 0;
-    sink_tiles = (s + DecCfg::kKeys - 1) / DecCfg::kKeys;
-    const int from = paged ? win_lo / DecCfg::kKeys * DecCfg::kKeys : win_lo;
-    win_base = from > sink_tiles * DecCfg::kKeys ? from : sink_tiles * DecCfg::kKeys;
-    return sink_tiles + (Nk > win_base ? (Nk - win_base + DecCfg::kKeys - 1) / DecCfg::kKeys : 0);
-}
-
 // NARROW: the head has fewer than 128 columns (p.d_io); the full-width kernel
 // compiles without the column checks.
-// WIN: sliding window with sinks (causal): only the 64-key tiles that hold a visible key are
-// read, first those of the sinks, then those from the first row's window on.
-// SCORES: the scores are also written out, for the weights that the keys receive.
-// LENS: a padded dense cache, sequence b holding its first seq_lens[b] keys.
-template <bool PAGED, typename T = __nv_bfloat16, bool NARROW = false, bool WIN = false, bool SCORES = false,
-          bool LENS = false>
+template <bool PAGED, typename T = __nv_bfloat16, bool NARROW = false>
 __global__ void __launch_bounds__(160, 2)   // two CTAs per SM (shared memory allows exactly two)
     decode_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         DecodeParams p)
@@ -125,28 +104,10 @@ __global__ void __launch_bounds__(160, 2)   // two CTAs per SM (shared memory al
     const int kvh = (int)blockIdx.x / p.splits;     // b * Hkv + kv head
     const int b = kvh / p.Hkv, hk = kvh % p.Hkv;
     // keys of this sequence (a paged sequence's own length, clamped to what its table can hold)
-    const int Nk_b = PAGED  ? max(0, min(__ldg(p.seq_lens + b), p.max_pages * p.page_size))
-                     : LENS ? max(0, min(__ldg(p.seq_lens + b), p.Nk))
-                            : p.Nk;
-    int k_begin = split * p.chunk;
-    int k_end = min(Nk_b, k_begin + p.chunk);
-    int n_tiles = k_end > k_begin ? (k_end - k_begin + C::kKeys - 1) / C::kKeys : 0;
-    // window: the first row's first window key, tiles of sinks, first key of the window's tiles
-    int win_lo = 0, sink_tiles = 0, win_base = 0;
-    if constexpr (WIN) {
-        const int total = dec_win_tiles(Nk_b, p.Nq, p.window, p.sinks, PAGED, win_lo, sink_tiles, win_base);
-        const int t0 = split * (p.chunk / C::kKeys);
-        n_tiles = max(0, min(total - t0, p.chunk / C::kKeys));
-        k_begin = t0 * C::kKeys;   // place in the list of tiles
-        k_end = Nk_b;
-    }
-    // first key of the CTA's tile t
-    auto tile_key = [&](int t) {
-        const int x = k_begin + t * C::kKeys;
-        if constexpr (WIN)
-            return x < sink_tiles * C::kKeys ? x : win_base + x - sink_tiles * C::kKeys;
-        return x;
-    };
+    const int Nk_b = PAGED ? max(0, min(__ldg(p.seq_lens + b), p.max_pages * p.page_size)) : p.Nk;
+    const int k_begin = split * p.chunk;
+    const int k_end = min(Nk_b, k_begin + p.chunk);
+    const int n_tiles = k_end > k_begin ? (k_end - k_begin + C::kKeys - 1) / C::kKeys : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
@@ -172,7 +133,7 @@ __global__ void __launch_bounds__(160, 2)   // two CTAs per SM (shared memory al
                 // the second 64-column panel only when the head has columns there
                 const bool two = d_io > 64;
                 mbar_arrive_expect_tx(&bar_full[slot], (two ? 4 : 2) * C::kPanelBytes);
-                const int key0 = tile_key(t);
+                const int key0 = k_begin + t * C::kKeys;
                 if (PAGED) {
                     // a 64-key tile never straddles a page (page_size is a multiple of 64);
                     // an out-of-range page id reads zeros (TMA bounds), never another buffer
@@ -227,14 +188,12 @@ __global__ void __launch_bounds__(160, 2)   // two CTAs per SM (shared memory al
             }
         }
     }
-    // per-row causal limit (last visible key) for the two rows this thread holds, and the
-    // first key of the row's window
-    int lim[2], low[2];
+    // per-row causal limit (last visible key) for the two rows this thread holds
+    int lim[2];
     for (int hr = 0; hr < 2; ++hr) {
         const int r = g + 8 * hr;
         const int i = (r < p.R) ? r % p.Nq : 0;
         lim[hr] = p.causal ? min(k_end - 1, i + Nk_b - p.Nq) : k_end - 1;
-        low[hr] = lim[hr] - p.window + 1;
     }
 
     float o[16][4];
@@ -270,40 +229,15 @@ __global__ void __launch_bounds__(160, 2)   // two CTAs per SM (shared memory al
             }
         }
         // mask: keys past the chunk / causal limit
-        const int key0 = tile_key(t) + key_w;
+        const int key0 = k_begin + t * C::kKeys + key_w;
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int key = key0 + nt * 8 + 2 * tq + (e & 1);
-                if (key > lim[e >> 1] || (WIN && key < low[e >> 1] && key >= p.sinks))
+                if (key > lim[e >> 1])
                     s[nt][e] = -INFINITY;
             }
-        if constexpr (WIN || LENS) {
-            // V rows of keys that no row sees (between the sinks and the window, or past the
-            // sequence in its last page or in the padding) are zeroed: whatever they hold, 0 * V adds nothing
-            if (key0 + 16 > Nk_b || (WIN && key0 < win_lo && key0 + 16 > p.sinks)) {
-                for (int i = lane; i < 256; i += 32) {
-                    const int key = key0 + (i >> 4);
-                    if (key >= Nk_b || (WIN && key >= p.sinks && key < win_lo))
-                        *reinterpret_cast<uint4*>(smem + C::kOffRing + slot * 2 * C::kTileBytes + C::kTileBytes +
-                                                  dec_tile_off(key_w + (i >> 4), i & 15)) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();   // before the slot is given back to the TMA
-                __syncwarp();
-            }
-        }
-        if constexpr (SCORES) {
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int hr = 0; hr < 2; ++hr) {
-                    const int r = g + 8 * hr;
-                    if (r < p.R)
-                        *reinterpret_cast<float2*>(p.scores + ((size_t)kvh * p.R + r) * p.score_stride + key0 +
-                                                   nt * 8 + 2 * tq) = make_float2(s[nt][2 * hr] * sl2, s[nt][2 * hr + 1] * sl2);
-                }
-        }
         // online softmax for rows g (e = 0, 1) and g + 8 (e = 2, 3)
         uint32_t pa[4];
 #pragma unroll
@@ -389,7 +323,7 @@ __global__ void __launch_bounds__(160, 2)   // two CTAs per SM (shared memory al
         }
         const float on = (L > 0.f) ? acc / L : 0.f;
         const float lse = (L > 0.f) ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
-        if (p.part_o == nullptr) {   // a single split, final
+        if (p.splits == 1) {
             const int h = hk * p.G + r / p.Nq, i = r % p.Nq;
             const size_t row = ((size_t)b * p.Hq + h) * p.Nq + i;
             if (dcol < d_io)

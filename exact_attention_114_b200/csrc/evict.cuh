@@ -6,7 +6,7 @@
 //                          saved LSE (the recomputation of P that the backward does, without its
 //                          gradients)
 //   key_weights_add_kernel adds the sums of a launch whose rows were shared between CTAs
-//   decode_weights_kernel  the same for the split-KV decode, from the scores it leaves behind
+//   (the split-KV decode leaves its scores behind instead: decode_weights_kernel)
 //   evict_select_kernel    the kept keys of each (batch, kv head), in order
 //   evict_gather_kernel    their rows of K and V, moved to the front of a new cache
 #pragma once
@@ -280,47 +280,6 @@ __global__ void __launch_bounds__(256) key_weights_add_kernel(KeyWeightParams p)
             s += p.part[(size_t)sp * n + i];
         p.w_out[i] = (p.w_in ? p.w_in[i] : 0.f) + s;
     }
-}
-
-// ----------------------------------------------------------------------------
-// decode: the split pass has left its scores (log2 units, -inf where masked) and
-// the partial log-sum-exps.  One block per 256 keys of a (batch, kv head).
-// ----------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) decode_weights_kernel(DecodeParams p)
-{
-    __shared__ float s_lse[16];
-    griddep_wait();
-    const int chunks = (p.Nk + 255) / 256;
-    const int kvh = (int)blockIdx.x / chunks, key = ((int)blockIdx.x % chunks) * 256 + (int)threadIdx.x;
-    const int warp = warp_id(), lane = lane_id();
-    for (int r = warp; r < p.R; r += 8) {
-        // the row's log-sum-exp over its splits (natural units), here in log2 units
-        const size_t base = (size_t)kvh * p.splits * p.R + r;
-        float M = -INFINITY;
-        for (int s = lane; s < p.splits; s += 32)
-            M = fmaxf(M, p.part_lse[base + (size_t)s * p.R]);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-        float L = 0.f;
-        if (M != -INFINITY)
-            for (int s = lane; s < p.splits; s += 32)
-                L += __expf(p.part_lse[base + (size_t)s * p.R] - M);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            L += __shfl_xor_sync(0xffffffffu, L, off);
-        if (lane == 0)
-            s_lse[r] = L > 0.f ? (M + __logf(L)) * 1.4426950408889634f : INFINITY;   // P = 0 in a row without keys
-    }
-    __syncthreads();
-    if (key >= p.Nk)
-        return;
-    float sum = 0.f;
-    const float* sc = p.scores + (size_t)kvh * p.R * p.score_stride + key;
-    for (int r = 0; r < p.R; ++r)
-        sum += ex2_approx(sc[(size_t)r * p.score_stride] - s_lse[r]);
-    const size_t at = (size_t)kvh * p.Nk + key;
-    p.w_out[at] = (p.w_in ? p.w_in[at] : 0.f) + sum;
 }
 
 // ----------------------------------------------------------------------------

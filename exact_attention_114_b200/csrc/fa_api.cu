@@ -23,10 +23,12 @@
 
 #include "bwd.cuh"
 #include "decode.cuh"
+#include "decode_stream.cuh"
 #include "evict.cuh"
 #include "fa_kernels.h"
 #include "fp8.cuh"
 #include "fwd.cuh"
+#include "prefix.cuh"
 
 namespace {
 
@@ -64,6 +66,26 @@ fa_status_t check_ptr(const void* p, const char* name)
     }
     if (!aligned16(p)) {
         set_error("%s is not 16-byte aligned", name);
+        return FA_ERR_INVALID_ARGUMENT;
+    }
+    return FA_OK;
+}
+
+fa_status_t check_float(const void* p, const char* name, bool may_be_null)
+{
+    if (!p && may_be_null)
+        return FA_OK;
+    if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) {
+        set_error("%s must be non-NULL and 4-byte aligned", name);
+        return FA_ERR_INVALID_ARGUMENT;
+    }
+    return FA_OK;
+}
+
+fa_status_t check_dtype(int dtype)
+{
+    if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_FP16) {
+        set_error("dtype=%d is not FA_DTYPE_BF16 or FA_DTYPE_FP16", dtype);
         return FA_ERR_INVALID_ARGUMENT;
     }
     return FA_OK;
@@ -744,17 +766,7 @@ int decode_splits(int B, int Hkv, int Nk, int requested)
 struct DecodePlan {
     int splits, chunk;
     size_t o_bytes, lse_bytes;
-    bool partial = false;   // partial results even of a single split
-    bool partials() const { return splits > 1 || partial; }
-    size_t total() const { return partials() ? align256(o_bytes) + align256(lse_bytes) : 0; }
-};
-
-// The keys' weights that a decode adds up (fa_fwd_weights)
-struct DecodeWeights {
-    const float* in;
-    float* out;
-    float* scores;
-    int stride;
+    size_t total() const { return splits > 1 ? align256(o_bytes) + align256(lse_bytes) : 0; }
 };
 
 DecodePlan decode_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d, int requested)
@@ -780,8 +792,7 @@ struct PagedDesc {
 template <typename T>
 fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
                             int Hkv, int Nq, int Nk, int d, float scale, int causal, const DecodePlan& pl, void* ws,
-                            cudaStream_t stream, const PagedDesc* pg, const Window* win, const DecodeWeights* dw,
-                            const int* lens, bool merge)
+                            cudaStream_t stream, const PagedDesc* pg)
 {
     using C = fa::DecCfg;
     CUtensorMap mk, mv;
@@ -795,23 +806,15 @@ fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o
     }
     auto kern = d < 128 ? (pg ? fa::decode_split_kernel<true, T, true> : fa::decode_split_kernel<false, T, true>)
                         : (pg ? fa::decode_split_kernel<true, T, false> : fa::decode_split_kernel<false, T, false>);
-    if (win)
-        kern = d < 128 ? (pg ? fa::decode_split_kernel<true, T, true, true> : fa::decode_split_kernel<false, T, true, true>)
-                       : (pg ? fa::decode_split_kernel<true, T, false, true> : fa::decode_split_kernel<false, T, false, true>);
-    if (dw)
-        kern = d < 128 ? fa::decode_split_kernel<false, T, true, false, true> : fa::decode_split_kernel<false, T, false, false, true>;
-    if (lens)
-        kern = d < 128 ? fa::decode_split_kernel<false, T, true, false, false, true>
-                       : fa::decode_split_kernel<false, T, false, false, false, true>;
     if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
-    fa::DecodeParams p = {};
+    fa::DecodeParams p;
     p.q = q;
     p.k = k;
     p.v = v;
     p.o = o;
     p.lse = lse;
-    p.part_o = pl.partials() ? static_cast<float*>(ws) : nullptr;
-    p.part_lse = pl.partials() ? reinterpret_cast<float*>(static_cast<char*>(ws) + align256(pl.o_bytes)) : nullptr;
+    p.part_o = pl.splits > 1 ? static_cast<float*>(ws) : nullptr;
+    p.part_lse = pl.splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(ws) + align256(pl.o_bytes)) : nullptr;
     p.B = B;
     p.Hq = Hq;
     p.Hkv = Hkv;
@@ -825,58 +828,28 @@ fa_status_t launch_decode_t(const void* q, const void* k, const void* v, void* o
     p.d_io = d;
     p.scale_log2 = scale * kLog2e;
     p.block_table = pg ? pg->block_table : nullptr;
-    p.seq_lens = pg ? pg->seq_lens : lens;
+    p.seq_lens = pg ? pg->seq_lens : nullptr;
     p.page_size = pg ? pg->page_size : 0;
     p.max_pages = pg ? pg->max_pages : 0;
-    p.window = win ? win->window : 0;
-    p.sinks = win ? win->sinks : 0;
-    if (dw) {
-        p.scores = dw->scores;
-        p.score_stride = dw->stride;
-        p.w_in = dw->in;
-        p.w_out = dw->out;
-    }
     const long long grid = (long long)B * Hkv * pl.splits;
     kern<<<(unsigned)grid, C::kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
     if ((st = check_launch("decode_split_kernel launch")) != FA_OK) return st;
-    if (pl.partials() && merge) {
+    if (pl.splits > 1) {
         const long long rows = (long long)B * Hkv * p.R;
         if ((st = launch_dependent("decode_combine_kernel launch", fa::decode_combine_kernel<T>,
                                    dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, p)) != FA_OK)
             return st;
-    }
-    if (dw) {
-        // launched plainly: the scores are two kernels back
-        const long long blocks = (long long)B * Hkv * ((Nk + 255) / 256);
-        fa::decode_weights_kernel<<<(unsigned)blocks, 256, 0, stream>>>(p);
-        return check_launch("decode_weights_kernel launch");
     }
     return FA_OK;
 }
 
 fa_status_t launch_decode(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
                           int Nq, int Nk, int d, float scale, int causal, const DecodePlan& pl, void* ws,
-                          cudaStream_t stream, const PagedDesc* pg = nullptr, int dtype = FA_DTYPE_BF16,
-                          const Window* win = nullptr, const DecodeWeights* dw = nullptr)
+                          cudaStream_t stream, const PagedDesc* pg = nullptr, int dtype = FA_DTYPE_BF16)
 {
     if (dtype == FA_DTYPE_FP16)
-        return launch_decode_t<__half>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, stream, pg, win,
-                                       dw, nullptr, true);
-    return launch_decode_t<__nv_bfloat16>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, stream, pg,
-                                          win, dw, nullptr, true);
-}
-
-// Keys of the longest list of visible tiles that a windowed decode may meet: Nk keys in a dense
-// cache, any length up to Nk in a paged one.
-int win_list_keys(int Nq, int Nk, const Window& w, bool paged)
-{
-    int lo, sink_tiles, base;
-    if (!paged)
-        return fa::DecCfg::kKeys * fa::dec_win_tiles(Nk, Nq, w.window, w.sinks, false, lo, sink_tiles, base);
-    // the window's keys start anywhere in their first tile
-    const int kt = fa::DecCfg::kKeys;
-    const long long tiles = (w.sinks + kt - 1) / kt + ((long long)w.window + Nq - 1 + kt - 2) / kt + 1;
-    return (int)std::min<long long>(tiles, (Nk + kt - 1) / kt) * kt;
+        return launch_decode_t<__half>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, stream, pg);
+    return launch_decode_t<__nv_bfloat16>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, stream, pg);
 }
 
 // ---------------------------------------------------------------------------
@@ -991,6 +964,214 @@ fa_status_t noalloc_scratch(void** out)
     }
     *out = addr[dev];
     return FA_OK;
+}
+
+// ---------------------------------------------------------------------------
+// split-KV over lists of keys (decode_stream.cuh)
+// ---------------------------------------------------------------------------
+struct StreamArgs {
+    int dtype;
+    const void *q, *k, *v;
+    void* o;
+    float* lse;
+    int B, Hq, Hkv, Nq, Nk, d;
+    float scale;
+    int causal;
+    int list;
+    Window win;                  // kListWindow, kListPaged
+    const int* lens;             // own lengths, or nullptr
+    const PagedDesc* pg;         // kListPaged
+    const void *k0, *v0;         // kListCat: the prefix, np keys
+    int np;
+    bool partial, after;
+    float* scores;               // with the keys' weights
+    int score_stride;
+};
+
+StreamArgs stream_args(int dtype, const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
+                       int Hkv, int Nq, int Nk, int d, float scale, int causal)
+{
+    StreamArgs a = {};
+    a.dtype = dtype;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.o = o;
+    a.lse = lse;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.Nq = Nq;
+    a.Nk = Nk;
+    a.d = d;
+    a.scale = scale;
+    a.causal = causal;
+    return a;
+}
+
+fa::StreamParams stream_params(const StreamArgs& a)
+{
+    fa::StreamParams p = {};
+    p.q = a.q;
+    p.o = a.o;
+    p.lse = a.lse;
+    p.seq_lens = a.lens;
+    p.B = a.B;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.Nq = a.Nq;
+    p.Nk = a.Nk;
+    p.G = a.Hq / a.Hkv;
+    p.R = p.G * a.Nq;
+    p.d_io = a.d;
+    p.causal = a.causal;
+    p.window = a.win.window;
+    p.sinks = a.win.sinks;
+    p.np = a.np;
+    p.partial = a.partial;
+    p.after = a.after;
+    p.scale_log2 = a.scale * kLog2e;
+    p.scores = a.scores;
+    p.score_stride = a.score_stride;
+    if (a.pg) {
+        p.block_table = a.pg->block_table;
+        p.page_size = a.pg->page_size;
+        p.max_pages = a.pg->max_pages;
+    }
+    return p;
+}
+
+struct StreamPlan {
+    int grid, tiles;
+    bool merge;     // units are cut, or may be empty
+    size_t lse_off, first_off, total;
+};
+
+// CTAs: two per SM where the line of tiles is long enough for at least two tiles each.  Lists of at
+// most 4 tiles stay whole if each can have a CTA of its own: the merge would take longer than the
+// tiles after the first.
+StreamPlan stream_plan(const StreamArgs& a)
+{
+    const fa::StreamParams p = stream_params(a);
+    StreamPlan pl;
+    switch (a.list) {
+    case fa::kListWindow: pl.tiles = fa::stream_list<fa::kListWindow>(p, a.Nk).tiles; break;
+    case fa::kListPaged: pl.tiles = fa::stream_list<fa::kListPaged>(p, a.Nk).tiles; break;
+    case fa::kListCat: pl.tiles = fa::stream_list<fa::kListCat>(p, a.Nk).tiles; break;
+    default: pl.tiles = fa::stream_list<fa::kListAll>(p, a.Nk).tiles; break;
+    }
+    const long long units = (long long)a.B * a.Hkv, T = units * pl.tiles, most = 2LL * sm_count();
+    if (pl.tiles <= 4 && units <= most)
+        pl.grid = (int)units;
+    else
+        pl.grid = (int)std::max<long long>(1, std::min(most, T / 2));
+    // of equal lists none is cut where every CTA's part is a number of whole ones
+    const bool whole = !a.lens && T % pl.grid == 0 && (T / pl.grid) % pl.tiles == 0;
+    pl.merge = !whole;
+    const size_t slots = a.partial || pl.merge ? 2 * (size_t)pl.grid + (a.partial ? (size_t)units : 0) : 0;
+    pl.lse_off = align256(slots * p.R * kDecodeWidth * 4);
+    pl.first_off = pl.lse_off + align256(slots * p.R * 4);
+    pl.total = pl.first_off + (a.lens ? align256(((size_t)a.B + 1) * 4) : 0);
+    return pl;
+}
+
+fa::StreamParts stream_parts(const StreamArgs& a, const StreamPlan& pl, void* ws)
+{
+    char* w = static_cast<char*>(ws);
+    fa::StreamParts q;
+    q.o = reinterpret_cast<const float*>(w);
+    q.lse = reinterpret_cast<const float*>(w + pl.lse_off);
+    q.first = a.lens ? reinterpret_cast<const int*>(w + pl.first_off) : nullptr;
+    q.tiles = pl.tiles;
+    q.B = a.B;
+    q.Hkv = a.Hkv;
+    q.R = a.Hq / a.Hkv * a.Nq;
+    q.grid = pl.grid;
+    q.partial = a.partial;
+    return q;
+}
+
+template <typename T>
+fa_status_t launch_stream(const StreamArgs& a, const StreamPlan& pl, void* ws, cudaStream_t stream)
+{
+    using C = fa::StreamCfg;
+    CUtensorMap mk, mv, mk0, mv0;
+    fa_status_t st;
+    constexpr CUtensorMapDataType dt = tma_type<T>();
+    const uint64_t units = (uint64_t)a.B * a.Hkv;
+    if (a.list == fa::kListPaged) {
+        if ((st = make_map_paged(&mk, a.k, a.d, a.Hkv, a.pg->page_size, a.pg->num_pages, dt)) != FA_OK) return st;
+        if ((st = make_map_paged(&mv, a.v, a.d, a.Hkv, a.pg->page_size, a.pg->num_pages, dt)) != FA_OK) return st;
+    } else {
+        if ((st = make_map(&mk, a.k, a.d, a.Nk, units, 64, dt)) != FA_OK) return st;
+        if ((st = make_map(&mv, a.v, a.d, a.Nk, units, 64, dt)) != FA_OK) return st;
+    }
+    if (a.list == fa::kListCat) {
+        if ((st = make_map(&mk0, a.k0, a.d, a.np, (uint64_t)a.Hkv, 64, dt)) != FA_OK) return st;
+        if ((st = make_map(&mv0, a.v0, a.d, a.np, (uint64_t)a.Hkv, 64, dt)) != FA_OK) return st;
+    } else {
+        mk0 = mk;
+        mv0 = mv;
+    }
+    const bool narrow = a.d < 128;
+    auto pick = [&](auto list, auto scores) {
+        constexpr int L = decltype(list)::value;
+        constexpr bool S = decltype(scores)::value;
+        return narrow ? fa::decode_stream_kernel<T, true, L, S> : fa::decode_stream_kernel<T, false, L, S>;
+    };
+    using No = std::false_type;
+    auto kern = a.list == fa::kListWindow  ? pick(std::integral_constant<int, fa::kListWindow>{}, No{})
+                : a.list == fa::kListPaged ? pick(std::integral_constant<int, fa::kListPaged>{}, No{})
+                : a.list == fa::kListCat   ? pick(std::integral_constant<int, fa::kListCat>{}, No{})
+                : a.scores                 ? pick(std::integral_constant<int, fa::kListAll>{}, std::true_type{})
+                                           : pick(std::integral_constant<int, fa::kListAll>{}, No{});
+    if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
+    fa::StreamParams p = stream_params(a);
+    char* w = static_cast<char*>(ws);
+    p.part_o = reinterpret_cast<float*>(w);
+    p.part_lse = reinterpret_cast<float*>(w + pl.lse_off);
+    p.first = reinterpret_cast<int*>(w + pl.first_off);
+    if (a.after) {
+        st = launch_dependent("decode_stream_kernel launch", kern, dim3((unsigned)pl.grid), dim3(C::kThreads),
+                              (size_t)C::kSmemBytes, stream, mk, mv, mk0, mv0, p);
+    } else {
+        kern<<<(unsigned)pl.grid, C::kThreads, C::kSmemBytes, stream>>>(mk, mv, mk0, mv0, p);
+        st = check_launch("decode_stream_kernel launch");
+    }
+    if (st != FA_OK || a.partial || !pl.merge)
+        return st;
+    const long long rows = (long long)units * p.R;
+    return launch_dependent("stream_combine_kernel launch", fa::stream_combine_kernel<T>, dim3((unsigned)((rows + 3) / 4)),
+                            dim3(128), 0, stream, stream_parts(a, pl, ws), a.o, a.lse, a.d);
+}
+
+fa_status_t launch_stream_any(const StreamArgs& a, const StreamPlan& pl, void* ws, cudaStream_t stream)
+{
+    return a.dtype == FA_DTYPE_FP16 ? launch_stream<__half>(a, pl, ws, stream)
+                                    : launch_stream<__nv_bfloat16>(a, pl, ws, stream);
+}
+
+// The pass and its merge, with the caller's workspace or scratch of its own.
+fa_status_t run_stream(const StreamArgs& a, void* workspace, size_t workspace_bytes, cudaStream_t s)
+{
+    const StreamPlan pl = stream_plan(a);
+    if (workspace && workspace_bytes < pl.total) {
+        set_error("workspace has %zu bytes, %zu needed", workspace_bytes, pl.total);
+        return FA_ERR_WORKSPACE;
+    }
+    void* ws = workspace;
+    if (!ws && pl.total > 0) {
+        cudaError_t e = scratch_alloc(&ws, pl.total, s);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "scratch allocation (split-KV partials)");
+    }
+    fa_status_t st = launch_stream_any(a, pl, ws, s);
+    if (ws && !workspace) {
+        cudaError_t e = cudaFreeAsync(ws, s);
+        if (e != cudaSuccess && st == FA_OK)
+            st = cuda_fail(e, "cudaFreeAsync");
+    }
+    return st;
 }
 
 // ---------------------------------------------------------------------------
@@ -1126,33 +1307,55 @@ fa_status_t launch_prefix_pack(const PrefixArgs& a, int shares, float* part_o, f
 }
 
 struct PrefixPlan {
-    bool pack, decode;      // packed prefix pass; own keys by the split-KV decode
+    bool pack;              // packed prefix pass, own keys apart, and a merge
+    bool decode;            // the split-KV pass for the own keys (not packed: for all keys)
     int shares;             // of the prefix pass
-    DecodePlan own;         // decode: its splits (else one share)
+    StreamArgs own;         // decode: that pass
+    StreamPlan own_plan;
     size_t a_lse, b_o, b_lse, total;   // workspace offsets (a_o at 0) and size; 0 without a merge
 };
 
-PrefixPlan prefix_plan(const PrefixArgs& a)
+StreamArgs prefix_stream(const PrefixArgs& a, int dtype)
+{
+    StreamArgs x = stream_args(dtype, a.q, a.k, a.v, a.o, a.lse, a.B, a.Hq, a.Hkv, a.Nq, a.Ns, a.d, a.scale, a.causal);
+    x.lens = a.lens;
+    return x;
+}
+
+PrefixPlan prefix_plan(const PrefixArgs& a, int dtype)
 {
     PrefixPlan pl = {};
     pl.pack = prefix_packs(a);
-    if (!pl.pack)
+    pl.decode = decode_shape(a.Hq, a.Hkv, a.Nq, a.d);
+    if (pl.decode)
+        pl.own = prefix_stream(a, dtype);
+    if (!pl.pack) {
+        if (pl.decode) {
+            pl.own.list = fa::kListCat;
+            pl.own.k0 = a.kp;
+            pl.own.v0 = a.vp;
+            pl.own.np = a.Np;
+            pl.own_plan = stream_plan(pl.own);
+            pl.total = pl.own_plan.total;
+        }
         return pl;
+    }
     const int rows = a.Hq / a.Hkv * a.Nq, pack = 128 / rows;
     const size_t total_rows = (size_t)a.B * a.Hq * a.Nq;
     const int kt = kernel_d(a.d) == 256 ? 1 : 2;
     const int tiles = (a.B + pack - 1) / pack;
     pl.shares = prefix_shares((long long)((tiles + kt - 1) / kt) * a.Hkv, (a.Np + 127) / 128, total_rows * a.d * 4.0,
                               sm_count());
-    pl.decode = decode_shape(a.Hq, a.Hkv, a.Nq, a.d);
-    pl.own = decode_plan(a.B, a.Hq, a.Hkv, a.Nq, a.Ns, a.d, pl.decode ? 0 : 1);
-    pl.own.partial = true;
     pl.a_lse = align256(total_rows * pl.shares * a.d * 4);
     pl.b_o = pl.a_lse + align256(total_rows * pl.shares * 4);
-    const size_t b_o_bytes = pl.decode ? pl.own.o_bytes : total_rows * a.d * 4;
-    const size_t b_lse_bytes = pl.decode ? pl.own.lse_bytes : total_rows * 4;
-    pl.b_lse = pl.b_o + align256(b_o_bytes);
-    pl.total = pl.b_lse + align256(b_lse_bytes);
+    if (pl.decode) {
+        pl.own.partial = pl.own.after = true;
+        pl.own_plan = stream_plan(pl.own);
+        pl.total = pl.b_o + pl.own_plan.total;
+    } else {
+        pl.b_lse = pl.b_o + align256(total_rows * a.d * 4);
+        pl.total = pl.b_lse + align256(total_rows * 4);
+    }
     return pl;
 }
 
@@ -1160,47 +1363,40 @@ template <int D, typename T>
 fa_status_t launch_prefix(const PrefixArgs& a, const PrefixPlan& pl, void* ws, cudaStream_t stream)
 {
     if (!pl.pack)
-        return launch_prefix_cat<D, T>(a, a.Np, nullptr, nullptr, stream);
+        return pl.decode ? launch_stream<T>(pl.own, pl.own_plan, ws, stream)
+                         : launch_prefix_cat<D, T>(a, a.Np, nullptr, nullptr, stream);
     char* w = static_cast<char*>(ws);
     float* a_o = reinterpret_cast<float*>(w);
     float* a_lse = reinterpret_cast<float*>(w + pl.a_lse);
-    float* b_o = reinterpret_cast<float*>(w + pl.b_o);
-    float* b_lse = reinterpret_cast<float*>(w + pl.b_lse);
     fa_status_t st = launch_prefix_pack<D, T>(a, pl.shares, a_o, a_lse, stream);
     if (st != FA_OK)
         return st;
-    const int rows = a.Hq / a.Hkv * a.Nq;
     fa::PrefixMerge m = {};
-    m.nb = 1;
-    m.b_ld = a.d;
-    m.b_unit = 1.f;
     if (pl.decode) {
-        if (a.lens)
-            st = launch_decode_t<T>(a.q, a.k, a.v, a.o, a.lse, a.B, a.Hq, a.Hkv, a.Nq, a.Ns, a.d, a.scale, a.causal, pl.own,
-                                    b_o, stream, nullptr, nullptr, nullptr, a.lens, false);
-        else
-            st = launch_decode_t<T>(a.q, a.k, a.v, a.o, a.lse, a.B, a.Hq, a.Hkv, a.Nq, a.Ns, a.d, a.scale, a.causal, pl.own,
-                                    b_o, stream, nullptr, nullptr, nullptr, nullptr, false);
-        m.nb = pl.own.splits;
+        if ((st = launch_stream<T>(pl.own, pl.own_plan, w + pl.b_o, stream)) != FA_OK)
+            return st;
+        m.own = stream_parts(pl.own, pl.own_plan, w + pl.b_o);
         m.b_ld = kDecodeWidth;
-        m.b_unit = kLog2e;
     } else {
-        st = launch_prefix_cat<D, T>(a, 0, b_o, b_lse, stream);
+        float* b_o = reinterpret_cast<float*>(w + pl.b_o);
+        float* b_lse = reinterpret_cast<float*>(w + pl.b_lse);
+        if ((st = launch_prefix_cat<D, T>(a, 0, b_o, b_lse, stream)) != FA_OK)
+            return st;
+        m.own.o = b_o;
+        m.own.lse = b_lse;
+        m.own.R = a.Hq / a.Hkv * a.Nq;
+        m.b_ld = a.d;
     }
-    if (st != FA_OK)
-        return st;
+    m.tiled = !pl.decode;
     m.a_o = a_o;
     m.a_lse = a_lse;
-    m.b_o = b_o;
-    m.b_lse = b_lse;
     m.na = pl.shares;
-    m.seq_rows = rows;
     m.d_io = a.d;
     m.rows = (long long)a.B * a.Hq * a.Nq;
     m.o = a.o;
     m.lse = a.lse;
-    fa::prefix_merge_kernel<T><<<(unsigned)((m.rows + 3) / 4), 128, 0, stream>>>(m);
-    return check_launch("prefix_merge_kernel launch");
+    return launch_dependent("prefix_merge_kernel launch", fa::prefix_merge_kernel<T>, dim3((unsigned)((m.rows + 3) / 4)),
+                            dim3(128), 0, stream, m);
 }
 
 template <typename T>
@@ -1484,26 +1680,6 @@ fa_status_t key_weights(int dtype, const void* q, const void* k, const float* ls
                                   : key_weights_t<__nv_bfloat16>(q, k, p, Hq / Hkv, d, s);
 }
 
-fa_status_t check_float(const void* p, const char* name, bool may_be_null)
-{
-    if (!p && may_be_null)
-        return FA_OK;
-    if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) {
-        set_error("%s must be non-NULL and 4-byte aligned", name);
-        return FA_ERR_INVALID_ARGUMENT;
-    }
-    return FA_OK;
-}
-
-fa_status_t check_dtype(int dtype)
-{
-    if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_FP16) {
-        set_error("dtype=%d is not FA_DTYPE_BF16 or FA_DTYPE_FP16", dtype);
-        return FA_ERR_INVALID_ARGUMENT;
-    }
-    return FA_OK;
-}
-
 bool overlap(const void* a, size_t na, const void* b, size_t nb)
 {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -1596,15 +1772,20 @@ static fa_status_t fwd_entry(int dtype, const void* q, const void* k, const void
                                           : fwd_win_t<__nv_bfloat16>(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, win, s);
         return fwd_tiled(dtype, q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, s);
     }
-    const DecodePlan pl = decode_plan(B, Hq, Hkv, Nq, window ? win_list_keys(Nq, Nk, win, false) : Nk, d, 0);
+    if (window) {
+        StreamArgs a = stream_args(dtype, q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, 1);
+        a.list = fa::kListWindow;
+        a.win = win;
+        return run_stream(a, nullptr, 0, s);
+    }
+    const DecodePlan pl = decode_plan(B, Hq, Hkv, Nq, Nk, d, 0);
     void* ws = nullptr;
     if (pl.total() > 0) {
         cudaError_t e = scratch_alloc(&ws, pl.total(), s);
         if (e != cudaSuccess)
             return cuda_fail(e, "scratch allocation (split-KV partials)");
     }
-    st = launch_decode(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, s, nullptr, dtype,
-                       window ? &win : nullptr);
+    st = launch_decode(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, s, nullptr, dtype);
     if (ws) {
         cudaError_t e = cudaFreeAsync(ws, s);
         if (e != cudaSuccess && st == FA_OK)
@@ -1806,7 +1987,7 @@ static fa_status_t paged_entry(int dtype, const void* q, const void* k_cache, co
                                const int* block_table, const int* seq_lens, void* o, float* lse, int B, int Hq,
                                int Hkv, int Nq, int d, int page_size, int num_pages, int max_pages_per_seq,
                                float scale, int causal, int num_splits, void* workspace, size_t workspace_bytes,
-                               void* stream, const int* window = nullptr)
+                               void* stream)
 {
     t_error.clear();
     fa_status_t st;
@@ -1847,11 +2028,7 @@ static fa_status_t paged_entry(int dtype, const void* q, const void* k_cache, co
         return FA_ERR_INVALID_ARGUMENT;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    Window win = {};
-    if (window && (st = check_window(window[0], window[1], max_len, &win)) != FA_OK)
-        return st;
-    const int plan_keys = window ? win_list_keys(Nq, max_len, win, true) : max_len;
-    const DecodePlan pl = decode_plan(B, Hq, Hkv, Nq, plan_keys, d, num_splits);
+    const DecodePlan pl = decode_plan(B, Hq, Hkv, Nq, max_len, d, num_splits);
     void* ws = workspace;
     bool owned = false;
     if (pl.total() > 0) {
@@ -1867,7 +2044,7 @@ static fa_status_t paged_entry(int dtype, const void* q, const void* k_cache, co
     }
     PagedDesc pg{block_table, seq_lens, page_size, num_pages, max_pages_per_seq};
     st = launch_decode(q, k_cache, v_cache, o, lse, B, Hq, Hkv, Nq, max_len, d, scale, causal, pl, ws, s, &pg,
-                       dtype, window ? &win : nullptr);
+                       dtype);
     if (owned) {
         cudaError_t e = cudaFreeAsync(ws, s);
         if (e != cudaSuccess && st == FA_OK)
@@ -2078,25 +2255,56 @@ fa_status_t fa_bwd_window(fa_dtype_t dtype, const void* q, const void* k, const 
 }
 
 size_t fa_fwd_paged_window_workspace_size(int B, int Hq, int Hkv, int Nq, int page_size, int max_pages_per_seq, int d,
-                                          int window, int sinks, int num_splits)
+                                          int window, int sinks)
 {
-    if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Hq % Hkv != 0 || d < 1 || num_splits < 0 || page_size < 1 ||
-        max_pages_per_seq < 1 || (long long)page_size * max_pages_per_seq > (1ll << 30) || window < 1 || sinks < 0)
+    if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Hq % Hkv != 0 || d < 1 || page_size < 1 || max_pages_per_seq < 1 ||
+        (long long)page_size * max_pages_per_seq > (1ll << 30) || window < 1 || sinks < 0)
         return 0;
     const int max_len = page_size * max_pages_per_seq;
-    const Window w{std::min(window, max_len), std::min(sinks, max_len)};
-    return decode_plan(B, Hq, Hkv, Nq, win_list_keys(Nq, max_len, w, true), d, num_splits).total();
+    static const int some = 0;
+    StreamArgs a = stream_args(FA_DTYPE_BF16, nullptr, nullptr, nullptr, nullptr, nullptr, B, Hq, Hkv, Nq, max_len, d, 1.f, 1);
+    a.list = fa::kListPaged;
+    a.win = {std::min(window, max_len), std::min(sinks, max_len)};
+    a.lens = &some;
+    return stream_plan(a).total;
 }
 
 fa_status_t fa_fwd_paged_window(fa_dtype_t dtype, const void* q, const void* k_cache, const void* v_cache,
                                 const int* block_table, const int* seq_lens, void* o, float* lse, int B, int Hq,
                                 int Hkv, int Nq, int d, int page_size, int num_pages, int max_pages_per_seq,
-                                float scale, int window, int sinks, int num_splits, void* workspace,
-                                size_t workspace_bytes, void* stream)
+                                float scale, int window, int sinks, void* workspace, size_t workspace_bytes,
+                                void* stream)
 {
-    const int w[2] = {window, sinks};
-    return paged_entry((int)dtype, q, k_cache, v_cache, block_table, seq_lens, o, lse, B, Hq, Hkv, Nq, d, page_size,
-                       num_pages, max_pages_per_seq, scale, 1, num_splits, workspace, workspace_bytes, stream, w);
+    t_error.clear();
+    fa_status_t st;
+    if ((st = check_dtype((int)dtype)) || (st = check_ptr(q, "q")) || (st = check_ptr(k_cache, "k_cache")) ||
+        (st = check_ptr(v_cache, "v_cache")) || (st = check_ptr(o, "o")) || (st = check_float(lse, "lse", true)) ||
+        (st = check_float(block_table, "block_table", false)) || (st = check_float(seq_lens, "seq_lens", false)))
+        return st;
+    if (page_size < 64 || page_size % 64 != 0 || num_pages < 1 || max_pages_per_seq < 1 ||
+        (long long)page_size * max_pages_per_seq > (1ll << 30) || (long long)num_pages * page_size > (1ll << 31)) {
+        set_error("page_size must be a positive multiple of 64; num_pages, max_pages_per_seq >= 1");
+        return FA_ERR_INVALID_ARGUMENT;
+    }
+    const int max_len = page_size * max_pages_per_seq;
+    if ((st = check_shape(B, Hq, Hkv, Nq, max_len, d, scale, 1)) != FA_OK)
+        return st;
+    PagedDesc pg{block_table, seq_lens, page_size, num_pages, max_pages_per_seq};
+    StreamArgs a = stream_args((int)dtype, q, k_cache, v_cache, o, lse, B, Hq, Hkv, Nq, max_len, d, scale, 1);
+    if ((st = check_window(window, sinks, max_len, &a.win)) != FA_OK)
+        return st;
+    if (!decode_shape(Hq, Hkv, Nq, d)) {
+        set_error("paged decode needs d <= 128 and Nq * Hq / Hkv <= %d", kDecodeMaxRows);
+        return FA_ERR_UNSUPPORTED;
+    }
+    if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)) {
+        set_error("workspace is not 256-byte aligned");
+        return FA_ERR_INVALID_ARGUMENT;
+    }
+    a.list = fa::kListPaged;
+    a.lens = seq_lens;
+    a.pg = &pg;
+    return run_stream(a, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 static bool prefix_sizes_ok(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d)
@@ -2108,7 +2316,10 @@ size_t fa_fwd_prefix_workspace_size(int B, int Hq, int Hkv, int Nq, int Np, int 
 {
     if (!prefix_sizes_ok(B, Hq, Hkv, Nq, Np, Ns, d))
         return 0;
-    return prefix_plan({nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, B, Hq, Hkv, Nq, Np, Ns, d, 1.f, 0})
+    // sized as with lengths, which take a little more
+    static const int some = 0;
+    return prefix_plan({nullptr, nullptr, nullptr, nullptr, nullptr, &some, nullptr, nullptr, B, Hq, Hkv, Nq, Np, Ns, d, 1.f, 0},
+                       FA_DTYPE_BF16)
         .total;
 }
 
@@ -2133,7 +2344,7 @@ fa_status_t fa_fwd_prefix(fa_dtype_t dtype, const void* q, const void* k_prefix,
         return FA_ERR_INVALID_ARGUMENT;
     }
     const PrefixArgs a{q, k_prefix, v_prefix, k, v, seq_lens, o, lse, B, Hq, Hkv, Nq, Np, Ns, d, scale, causal};
-    const PrefixPlan pl = prefix_plan(a);
+    const PrefixPlan pl = prefix_plan(a, (int)dtype);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void* ws = workspace;
     if (workspace && workspace_bytes < pl.total) {
@@ -2182,17 +2393,33 @@ fa_status_t fa_fwd_weights(fa_dtype_t dtype, const void* q, const void* k, const
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void* ws = nullptr;
     if (decode_shape(Hq, Hkv, Nq, d)) {
-        DecodePlan pl = decode_plan(B, Hq, Hkv, Nq, Nk, d, 0);
-        pl.partial = true;
-        const int stride = (Nk + 63) / 64 * 64;
-        const size_t need = pl.total() + (size_t)B * Hq * Nq * stride * 4;
-        cudaError_t e = scratch_alloc(&ws, need, s);
+        StreamArgs a = stream_args((int)dtype, q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal);
+        const StreamPlan pl = stream_plan(a);
+        const size_t rows = (size_t)B * Hq * Nq, stride = ((size_t)Nk + 63) / 64 * 64;
+        const size_t lse_off = pl.total + align256(rows * stride * 4);
+        cudaError_t e = scratch_alloc(&ws, lse_off + (lse ? 0 : rows * 4), s);
         if (e != cudaSuccess)
             return cuda_fail(e, "scratch allocation (decode partials and scores)");
-        const DecodeWeights dw{weights_in, weights_out, reinterpret_cast<float*>(static_cast<char*>(ws) + pl.total()),
-                               stride};
-        st = launch_decode(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal, pl, ws, s, nullptr, (int)dtype,
-                           nullptr, &dw);
+        char* w = static_cast<char*>(ws);
+        a.scores = reinterpret_cast<float*>(w + pl.total);
+        a.score_stride = (int)stride;
+        if (!lse)
+            a.lse = reinterpret_cast<float*>(w + lse_off);
+        st = launch_stream_any(a, pl, ws, s);
+        if (st == FA_OK) {
+            fa::DecodeWeightParams p;
+            p.scores = a.scores;
+            p.lse = a.lse;
+            p.w_in = weights_in;
+            p.w_out = weights_out;
+            p.BH = B * Hkv;
+            p.R = Hq / Hkv * Nq;
+            p.Nk = Nk;
+            p.stride = a.score_stride;
+            const long long blocks = (long long)p.BH * ((Nk + 511) / 512);
+            st = launch_dependent("decode_weights_kernel launch", fa::decode_weights_kernel, dim3((unsigned)blocks),
+                                  dim3(128), 0, s, p);
+        }
     } else {
         float* l = lse;
         if (!l) {

@@ -99,15 +99,6 @@ struct DecodeParams {
     const int* seq_lens;     // [B]
     int page_size;
     int max_pages;
-    // sliding window with sinks (decode_split_kernel<..., WIN = true>), as in FwdParams;
-    // `chunk` then counts keys of the visible tiles' list
-    int window;
-    int sinks;
-    // scores kept for the keys' weights (decode_split_kernel<..., SCORES = true>)
-    float* scores;       // [B * Hkv, R, score_stride]: scale * log2(e) * q.k, -inf where masked
-    int score_stride;    // Nk rounded up to whole tiles
-    const float* w_in;   // [B, Hkv, Nk] or nullptr (zeros)
-    float* w_out;        // [B, Hkv, Nk]
 };
 
 struct BwdParams {

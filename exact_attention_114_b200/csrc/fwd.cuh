@@ -1127,85 +1127,4 @@ __global__ void __launch_bounds__(128) fwd_combine_kernel(FwdParams p)
         p.lse[row] = (L > 0.f) ? (M + __log2f(L)) * kLn2 : -INFINITY;
 }
 
-// Merge of a shared prefix's partials with those of the own keys (one warp per query row), the
-// rescale-and-add of the online softmax as in fwd_combine_kernel: na shares of the prefix pass
-// ([na][rows]) and nb shares of the own keys' pass ([batch * kv heads][nb][seq_rows], from the tiled
-// forward or from the split-KV decode).
-struct PrefixMerge {
-    const float* a_o;
-    const float* a_lse;    // log2 units
-    const float* b_o;
-    const float* b_lse;    // times b_unit: log2 units
-    float b_unit;
-    int na, nb, b_ld;      // b_ld: floats per row of b_o
-    int seq_rows, d_io;
-    long long rows;
-    void* o;
-    float* lse;
-};
-
-template <typename T>
-__global__ void __launch_bounds__(128) prefix_merge_kernel(PrefixMerge p)
-{
-    griddep_wait();
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= p.rows)
-        return;
-    const long long bh = row / p.seq_rows, r = row % p.seq_rows;
-    const int n = p.na + p.nb;
-    auto lse_of = [&](int s) {
-        return s < p.na ? p.a_lse[s * p.rows + row] : p.b_lse[(bh * p.nb + s - p.na) * p.seq_rows + r] * p.b_unit;
-    };
-    float M = -INFINITY;
-    for (int s = lane; s < n; s += 32)
-        M = fmaxf(M, lse_of(s));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    // lane l merges columns [c l, c l + c), c = d_io / 32
-    const int c = p.d_io / 32;
-    float acc[8], L = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        acc[k] = 0.f;
-    for (int s0 = 0; s0 < n && M != -INFINITY; s0 += 32) {
-        const float wl = s0 + lane < n ? ex2_approx(lse_of(s0 + lane) - M) : 0.f;
-#pragma unroll 4
-        for (int s = s0; s < min(n, s0 + 32); ++s) {
-            const float w = __shfl_sync(0xffffffffu, wl, s - s0);
-            if (w == 0.f)   // no key there (its O was never written) or a negligible share
-                continue;
-            L += w;
-            const float* o = (s < p.na ? p.a_o + (s * p.rows + row) * p.d_io
-                                       : p.b_o + ((bh * p.nb + s - p.na) * p.seq_rows + r) * p.b_ld) + c * lane;
-            if (c == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(o);
-                acc[0] = fmaf(w, v.x, acc[0]);
-                acc[1] = fmaf(w, v.y, acc[1]);
-                acc[2] = fmaf(w, v.z, acc[2]);
-                acc[3] = fmaf(w, v.w, acc[3]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < c)
-                        acc[k] = fmaf(w, o[k], acc[k]);
-            }
-        }
-    }
-    const float inv = (L > 0.f) ? 1.f / L : 0.f;
-    T* o = static_cast<T*>(p.o) + row * p.d_io + c * lane;
-    if (c == 4) {
-        *reinterpret_cast<uint2*>(o) = make_uint2(Elt<T>::pack(acc[0] * inv, acc[1] * inv),
-                                                  Elt<T>::pack(acc[2] * inv, acc[3] * inv));
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < c)
-                o[k] = Elt<T>::from_float(acc[k] * inv);
-    }
-    if (lane == 0 && p.lse)
-        p.lse[row] = (L > 0.f) ? (M + __log2f(L)) * kLn2 : -INFINITY;
-}
-
 }  // namespace fa

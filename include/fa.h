@@ -355,17 +355,18 @@ fa_status_t fa_bwd_window(fa_dtype_t dtype, const void* q, const void* k, const 
 
 /*
  * fa_fwd_window over a paged KV cache: arguments as fa_fwd_paged_ex (causal),
- * with the window against each sequence's own length.  Pages that hold no
+ * with the window against each sequence's own length; the work is spread over
+ * the SMs by the sequences' visible keys (no split count to give).  Pages that hold no
  * visible key are not read (their table entries may be anything), and what a
  * sequence's last page holds past its length does not matter.
  */
 size_t fa_fwd_paged_window_workspace_size(int B, int Hq, int Hkv, int Nq, int page_size, int max_pages_per_seq,
-                                          int d, int window, int sinks, int num_splits);
+                                          int d, int window, int sinks);
 fa_status_t fa_fwd_paged_window(fa_dtype_t dtype, const void* q, const void* k_cache, const void* v_cache,
                                 const int* block_table, const int* seq_lens, void* o, float* lse, int B, int Hq,
                                 int Hkv, int Nq, int d, int page_size, int num_pages, int max_pages_per_seq,
-                                float scale, int window, int sinks, int num_splits, void* workspace,
-                                size_t workspace_bytes, void* stream);
+                                float scale, int window, int sinks, void* workspace, size_t workspace_bytes,
+                                void* stream);
 
 /*
  * Forward of a batch whose sequences share a prefix (a common system prompt or

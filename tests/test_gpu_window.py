@@ -161,7 +161,7 @@ def test_backward_repeats_and_workspaces(shared):
 
 # shapes whose plans differ: the units of the sinks' blocks shared, the others, both, neither
 SPLITS = [((1, 8, 1, 1500, 1500, 64, 1400, 4), True, True), ((1, 2, 1, 4000, 4000, 64, 130, 4), False, True),
-          ((1, 32, 8, 8192, 8192, 64, 4096, 4), True, False), ((2, 8, 8, 1000, 1000, 64, 200, 1), False, False),
+          ((1, 32, 8, 8192, 8192, 64, 4096, 4), True, False), ((2, 8, 8, 1000, 1000, 64, 200, 0), False, False),
           ((1, 8, 1, 2048, 2048, 64, 512, 0), True, False)]
 
 
@@ -229,13 +229,15 @@ PAGED = [
     (8, 2, 1, 128, 64, [1, 700, 300, 0], 128, 4), (8, 8, 1, 64, 128, [1000, 65], 64, 0),
     (4, 1, 4, 128, 64, [3, 200, 129], 33, 70), (16, 1, 1, 96, 256, [5000], 2000, 1),
     (8, 2, 2, 128, 64, [640, 64, 1], 100000, 0), (8, 2, 1, 32, 64, [640, 641], 1, 1),
+    # lists longer than the GPU's CTAs, cut anywhere; more sequences than threads; empty ones between
+    (16, 4, 1, 128, 64, [9000, 0, 64, 8000, 1], 5000, 130), (4, 2, 1, 64, 64, [(37 * i) % 200 for i in range(300)], 70, 3),
+    (32, 8, 1, 128, 64, [2000 + i for i in range(64)], 1024, 4), (2, 1, 8, 128, 64, [0, 0, 5], 100, 0), (2, 2, 1, 64, 64, [0, 0], 3, 3),
 ]
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
-@pytest.mark.parametrize("splits", [0, 1, 5])
 @pytest.mark.parametrize("case", PAGED, ids=str)
-def test_paged(case, splits, dtype):
+def test_paged(case, dtype):
     Hq, Hkv, Nq, d, page, lens, window, sinks = case
     B, Nk = len(lens), max(max(lens), 1)
     q, k, v, _ = make(B, Hq, Hkv, Nq, Nk, d, dtype, 700 + PAGED.index(case))
@@ -244,7 +246,7 @@ def test_paged(case, splits, dtype):
     for b, n in enumerate(lens):   # pages behind the sinks and before the window: given to others
         for t in range(-(-sinks // page), max(0, n - Nq - window + 1) // page):
             table[b, t] = 10 ** 6 if t % 2 else -1
-    o, lse = fa.fa_fwd_paged_window(q, kp, vp, table, ln, window, sinks, num_splits=splits)
+    o, lse = fa.fa_fwd_paged_window(q, kp, vp, table, ln, window, sinks)
     torch.cuda.synchronize()
     fa.fa_check_device_status()
     for b, n in enumerate(lens):
@@ -260,14 +262,14 @@ def test_paged_workspace_and_outputs_given():
     q, k, v, _ = make(2, 8, 2, 1, 900, 128, BF16, 900)
     kp, vp, table = paged(k, v, [900, 800], 64, 901)
     ln = torch.tensor([900, 800], dtype=torch.int32, device="cuda")
-    need = fa.fa_fwd_paged_window_workspace_size(2, 8, 2, 1, 64, table.shape[1], 128, 300, 4, 3)
+    need = fa.fa_fwd_paged_window_workspace_size(2, 8, 2, 1, 64, table.shape[1], 128, 300, 4)
     o, lse = torch.empty_like(q), torch.empty(2, 8, 1, device="cuda")
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
-    fa.fa_fwd_paged_window(q, kp, vp, table, ln, 300, 4, o, lse, num_splits=3, workspace=ws)
-    o2, l2 = fa.fa_fwd_paged_window(q, kp, vp, table, ln, 300, 4, num_splits=3)
+    fa.fa_fwd_paged_window(q, kp, vp, table, ln, 300, 4, o, lse, workspace=ws)
+    o2, l2 = fa.fa_fwd_paged_window(q, kp, vp, table, ln, 300, 4)
     assert need > 0 and torch.equal(o, o2) and torch.equal(lse, l2)
     with pytest.raises(fa.FaError) as e:
-        fa.fa_fwd_paged_window(q, kp, vp, table, ln, 300, 4, num_splits=3, workspace=ws[:-256].contiguous())
+        fa.fa_fwd_paged_window(q, kp, vp, table, ln, 300, 4, workspace=ws[:-256].contiguous())
     assert e.value.status == fa.FA_ERR_WORKSPACE
 
 

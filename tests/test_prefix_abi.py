@@ -29,7 +29,7 @@ def test_refuses(kw, status):
 
 def test_workspace_sizes():
     assert fa.fa_fwd_prefix_workspace_size(4, 8, 2, 1, 500, 64, 128) > 4 * 8 * 128 * 4
-    assert fa.fa_fwd_prefix_workspace_size(1, 8, 2, 1, 500, 64, 128) == 0      # one sequence: nothing to merge
+    assert fa.fa_fwd_prefix_workspace_size(1, 8, 2, 17, 500, 64, 128) == 0     # one sequence: one launch of tiles
     assert fa.fa_fwd_prefix_workspace_size(4, 8, 2, 64, 500, 64, 128) == 0     # a sequence's rows fill a tile
     assert fa.fa_fwd_prefix_workspace_size(4, 8, 2, 1, 0, 64, 128) == 0
 

@@ -61,9 +61,9 @@ def test_workspace_holds_every_partial(shape):
 
 
 def test_paged_refuses():
-    def call(window=10, sinks=0, page=64, Nq=1, d=128, table=FAKE, ws=None, n=0, splits=0):
+    def call(window=10, sinks=0, page=64, Nq=1, d=128, table=FAKE, ws=None, n=0):
         return fa.lib().fa_fwd_paged_window(0, FAKE, FAKE, FAKE, table, FAKE, FAKE, None, 2, 8, 2, Nq, d, page, 100,
-                                            20, 0.1, window, sinks, splits, ws, n, None)
+                                            20, 0.1, window, sinks, ws, n, None)
 
     assert call(window=0) == fa.FA_ERR_INVALID_ARGUMENT
     assert call(sinks=-1) == fa.FA_ERR_INVALID_ARGUMENT
@@ -71,9 +71,9 @@ def test_paged_refuses():
     assert call(table=None) == fa.FA_ERR_INVALID_ARGUMENT
     assert call(Nq=8) == fa.FA_ERR_UNSUPPORTED
     assert call(d=256) == fa.FA_ERR_UNSUPPORTED
-    need = fa.fa_fwd_paged_window_workspace_size(2, 8, 2, 1, 64, 20, 128, 500, 4, 3)
-    assert need > 0 and call(window=500, sinks=4, splits=3, ws=ctypes.c_void_p(0x100000), n=need - 16) == fa.FA_ERR_WORKSPACE
-    assert fa.fa_fwd_paged_window_workspace_size(2, 8, 2, 1, 64, 20, 128, 0, 4, 3) == 0
+    need = fa.fa_fwd_paged_window_workspace_size(2, 8, 2, 1, 64, 20, 128, 500, 4)
+    assert need > 0 and call(window=500, sinks=4, ws=ctypes.c_void_p(0x100000), n=need - 16) == fa.FA_ERR_WORKSPACE
+    assert fa.fa_fwd_paged_window_workspace_size(2, 8, 2, 1, 64, 20, 128, 0, 4) == 0
 
 
 def test_binding_refuses():
