@@ -3,9 +3,10 @@
 // prefix followed by own keys.  The recurrence and the warp MMAs are those of the split pass in
 // decode.cuh; what differs is how the work is cut.
 //
-// Each (batch, kv head) is a unit: a list of 64-key tiles that hold at least one visible key.  The
-// tiles of all units form one line, T tiles long, and CTA c of G takes the tiles
-// [c T / G, (c + 1) T / G): as many as any other, whatever the lengths.  Its TMA warp runs through
+// Each (batch, kv head) is a unit: a list of 64-key tiles that hold at least one visible key.  All
+// units form one line, a place per tile and two more per unit (what ending one costs in tiles), T
+// places long, and CTA c of G takes the places [c T / G, (c + 1) T / G): as much work as any other,
+// whatever the lengths.  Its TMA warp runs through
 // them without a pause, into the next unit while the other warps still end the last one, so the
 // loads in flight (three stages of 32 KB, two CTAs per SM) never drain at a unit's end.  The pass is
 // bound by HBM, and short lists (a window of 1024 keys is 17 tiles) would otherwise spend a third of
@@ -14,9 +15,10 @@
 // A unit within one CTA is written out straight away.  A unit that continues in other CTAs leaves a
 // partial (O_s normalised, lse_s, fp32) in each: in the CTA's slot 1 where the CTA starts the unit, in
 // its slot 0 where it goes on with one, so two slots per CTA are enough.  Which CTAs hold a unit
-// follows from T, G and the unit's first tile, and stream_combine_kernel merges them in order.
+// follows from T, G and the unit's first place, and stream_combine_kernel merges them in order.
 #pragma once
 
+#include "bwd.cuh"   // bulk_load
 #include "decode.cuh"
 
 namespace fa {
@@ -33,7 +35,7 @@ struct StreamParams {
     float* lse;             // [B, Hq, Nq] or nullptr
     float* part_o;          // [slots][R][128]: 2 per CTA, then (partial) one per unit
     float* part_lse;        // [slots][R], log2 units
-    int* first;             // [B + 1] tiles of the sequences before b, per kv head (with lengths)
+    int* first;             // [B + 1] places of the sequences before b, per kv head (with lengths)
     const int* seq_lens;    // [B] or nullptr (Nk each)
     const int* block_table; // [B, max_pages] (kListPaged)
     int B, Hq, Hkv, Nq, Nk, G, R, d_io;
@@ -55,8 +57,10 @@ struct StreamCfg {
     static constexpr int kMergeRows = 4;               // rows of the four warps' states merged at a time
     static constexpr int kOffMerge = kStages * 2 * DecCfg::kTileBytes;
     static constexpr int kOffML = kOffMerge + 4 * kMergeRows * 128 * 4;   // [4 warps][16] m, then l
-    static constexpr int kOffScan = kOffML + 2 * 64 * 4;                  // [128] ints
-    static constexpr int kOffBar = kOffScan + 128 * 4;
+    static constexpr int kOffQ = kOffML + 2 * 64 * 4;                     // query rows of the next units
+    static constexpr int kQBytes = 16 * 128 * 2;
+    static constexpr int kQSlots = 4;                                     // at most (fewer where rows are many)
+    static constexpr int kOffBar = kOffQ + kQBytes;
     static constexpr int kSmemBytes = kOffBar + 128 + 1024;
     static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 };
@@ -100,7 +104,12 @@ __device__ __forceinline__ int stream_len(const StreamParams& p, int b)
     return p.seq_lens ? max(0, min(__ldg(p.seq_lens + b), p.Nk)) : p.Nk;
 }
 
-// The CTA that holds tile t of T, and CTA c's first tile.  Where the lengths leave fewer tiles than
+// Places of a unit with n tiles: a unit's end (the warps' merge, its stores, the next unit's start)
+// takes about as long as two tiles.
+constexpr int kUnitPlaces = 2;
+__host__ __device__ __forceinline__ int stream_places(int n) { return n > 0 ? n + kUnitPlaces : 0; }
+
+// The CTA that holds place t of T, and CTA c's first place.  Where the lengths leave fewer places than
 // CTAs were launched, T of them take one each (none between two of a unit's CTAs is empty).
 __host__ __device__ __forceinline__ int stream_cta(long long t, long long T, int grid)
 {
@@ -113,22 +122,29 @@ __host__ __device__ __forceinline__ long long stream_tile(int c, long long T, in
     return c < g ? c * T / g : T;
 }
 
-// Place in the line: kv head hk of sequence b, tile t of its list.
+// A CTA's walk along its part of the line: `left` places from place `off` of the unit (b, hk) on.
 template <int LIST>
-struct StreamPos {
-    int b, hk, t;
+struct StreamWalk {
+    int b, hk, off, left;
     StreamList l;
-    __device__ __forceinline__ void next_unit(const StreamParams& p)
+    // the unit's tiles in the part: [off, end())
+    __device__ __forceinline__ int end() const { return min(l.tiles, off + left); }
+    // on to the next unit with tiles; false at the part's end
+    __device__ __forceinline__ bool next(const StreamParams& p)
     {
-        t = 0;
+        left -= stream_places(l.tiles) - off;
+        off = 0;
+        if (left <= 0)
+            return false;
         if (++hk < p.Hkv)
-            return;
+            return true;
         hk = 0;
         do {
             if (++b >= p.B)
-                return;
+                return false;
             l = stream_list<LIST>(p, stream_len(p, b));
         } while (l.tiles == 0);
+        return true;
     }
 };
 
@@ -147,8 +163,9 @@ __global__ void __launch_bounds__(160, 2)
     uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     uint64_t* bar_empty = bar_full + C::kStages;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_empty + C::kStages);
-    int* start = const_cast<int*>(abort_flag) + 1;   // [3] b, hk, t of the CTA's first tile
-    int* scan = reinterpret_cast<int*>(smem + C::kOffScan);
+    uint64_t* bar_qfree = bar_empty + C::kStages + 1;   // [kQSlots] a unit's query rows are in registers (count 4)
+    int* start = reinterpret_cast<int*>(bar_qfree + C::kQSlots);   // [3] b, hk, t of the CTA's first tile
+    int* warp_sum = start + 3;                            // [4] tiles of the sequences of each warp's threads
 
     const int warp = warp_id(), lane = lane_id();
     const int cta = (int)blockIdx.x, grid = (int)gridDim.x;
@@ -157,6 +174,8 @@ __global__ void __launch_bounds__(160, 2)
             mbar_init(&bar_full[s], 1);
             mbar_init(&bar_empty[s], 4);
         }
+        for (int s = 0; s < C::kQSlots; ++s)
+            mbar_init(&bar_qfree[s], 4);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -166,52 +185,60 @@ __global__ void __launch_bounds__(160, 2)
     }
     // the line's length and the CTA's part of it
     long long total;
-    StreamPos<LIST> at;
+    StreamWalk<LIST> at;
     if (p.seq_lens == nullptr) {
         at.l = stream_list<LIST>(p, p.Nk);
-        total = (long long)at.l.tiles * p.B * p.Hkv;
+        const int n = stream_places(at.l.tiles);
+        total = (long long)n * p.B * p.Hkv;
         const long long t0 = stream_tile(cta, total, grid);
-        const int unit = (int)(t0 / at.l.tiles);
+        const int unit = (int)(t0 / n);
         at.b = unit / p.Hkv;
         at.hk = unit % p.Hkv;
-        at.t = (int)(t0 % at.l.tiles);
+        at.off = (int)(t0 % n);
         __syncthreads();
     } else {
-        // thread i of the first 128 sums the tiles of its share of the sequences
+        // thread i of the first 128 takes a share of the sequences (their places in registers where it
+        // has at most 4)
         const int per = (p.B + 127) / 128;
         const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
-        int mine = 0;
-        if (threadIdx.x < 128) {
-            for (int b = b0; b < b1; ++b)
-                mine += stream_list<LIST>(p, stream_len(p, b)).tiles;
-            scan[threadIdx.x] = mine;
-        }
-        __syncthreads();
-        if (warp == 0) {
-            int v[4], sum = 0;
-            for (int k = 0; k < 4; ++k) {
-                v[k] = sum;
-                sum += scan[4 * lane + k];
+        int mine = 0, before = 0, n4[4] = {0, 0, 0, 0};
+        if (warp < 4) {
+            if (per <= 4) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (b0 + k < b1)
+                        n4[k] = stream_places(stream_list<LIST>(p, stream_len(p, b0 + k)).tiles);
+                mine = n4[0] + n4[1] + n4[2] + n4[3];
+            } else {
+                for (int b = b0; b < b1; ++b)
+                    mine += stream_places(stream_list<LIST>(p, stream_len(p, b)).tiles);
             }
-            int incl = sum;
+            before = mine;
+#pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, incl, off);
+                const int x = __shfl_up_sync(0xffffffffu, before, off);
                 if (lane >= off)
-                    incl += x;
+                    before += x;
             }
-            __syncwarp();
-            for (int k = 0; k < 4; ++k)
-                scan[4 * lane + k] = v[k] + incl - sum;   // tiles before thread 4 lane + k's share
             if (lane == 31)
-                start[3] = incl;
+                warp_sum[warp] = before;
+            before -= mine;
         }
         __syncthreads();
-        total = (long long)start[3] * p.Hkv;
+        int all = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            before += k < warp ? warp_sum[k] : 0;
+            all += warp_sum[k];
+        }
+        total = (long long)all * p.Hkv;
         const long long t0 = stream_tile(cta, total, grid);
-        if (threadIdx.x < 128) {
-            int before = scan[threadIdx.x];
+        if (warp < 4) {
             for (int b = b0; b < b1; ++b) {
-                const int n = stream_list<LIST>(p, stream_len(p, b)).tiles;
+                const int n = per <= 4 ? n4[0] : stream_places(stream_list<LIST>(p, stream_len(p, b)).tiles);
+                n4[0] = n4[1];
+                n4[1] = n4[2];
+                n4[2] = n4[3];
                 if (cta == 0)
                     p.first[b] = before;   // for the merge
                 const long long lo = (long long)before * p.Hkv;
@@ -223,53 +250,70 @@ __global__ void __launch_bounds__(160, 2)
                 before += n;
             }
             if (cta == 0 && threadIdx.x == 127)
-                p.first[p.B] = start[3];
+                p.first[p.B] = all;
         }
         __syncthreads();
         at.b = start[0];
         at.hk = start[1];
-        at.t = start[2];
+        at.off = start[2];
         if (t0 < total)
             at.l = stream_list<LIST>(p, stream_len(p, at.b));
     }
-    const int n_mine = (int)(stream_tile(cta + 1, total, grid) - stream_tile(cta, total, grid));   // tiles of the CTA
-    int left = n_mine;
+    at.left = (int)(stream_tile(cta + 1, total, grid) - stream_tile(cta, total, grid));
+    const bool any = at.left > 0;
+
+    // slots for the units' query rows, so that the loads run ahead over units of a tile or two
+    const int q_bytes = p.R * d_io * 2;
+    const int q_slots = q_bytes * 4 <= C::kQBytes ? 4 : q_bytes * 2 <= C::kQBytes ? 2 : 1;
 
     if (warp == 4) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
             const bool two = d_io > 64;   // the second 64-column panel only when the head has columns there
             const uint32_t bytes = (uint32_t)(two ? 4 : 2) * DecCfg::kPanelBytes;
-            int n = 0;
-            for (; left > 0; --left, ++n) {
-                const int slot = n % C::kStages;
-                if (!mbar_wait(&bar_empty[slot], ((uint32_t)(n / C::kStages) & 1u) ^ 1u, abort_flag))
-                    break;
-                uint8_t* dk = smem + slot * 2 * DecCfg::kTileBytes;
-                uint8_t* dv = dk + DecCfg::kTileBytes;
-                mbar_arrive_expect_tx(&bar_full[slot], bytes);
-                const bool head_seg = at.t < at.l.seg;
-                const int key0 = head_seg ? at.t * kt : at.l.base + (at.t - at.l.seg) * kt;
-                if constexpr (LIST == kListPaged) {
-                    // an out-of-range page id reads zeros (TMA bounds), never another buffer
-                    const int page = __ldg(p.block_table + (size_t)at.b * p.max_pages + key0 / p.page_size);
-                    const int off = key0 % p.page_size;
-                    for (int pn = 0; pn < (two ? 2 : 1); ++pn) {
-                        tma_load_4d(dk + pn * DecCfg::kPanelBytes, &tmK, &bar_full[slot], pn * 64, at.hk, off, page);
-                        tma_load_4d(dv + pn * DecCfg::kPanelBytes, &tmV, &bar_full[slot], pn * 64, at.hk, off, page);
+            int n = 0, units = 0;
+            bool go = any;
+            while (go) {
+                const int t0 = at.off, t1 = at.end();
+                for (int t = t0; go && t < t1; ++t, ++n) {
+                    const int slot = n % C::kStages;
+                    go = mbar_wait(&bar_empty[slot], ((uint32_t)(n / C::kStages) & 1u) ^ 1u, abort_flag);
+                    // the unit's query rows come with its first tile
+                    if (go && t == t0)
+                        go = mbar_wait(&bar_qfree[units % q_slots], ((uint32_t)(units / q_slots) & 1u) ^ 1u, abort_flag);
+                    if (!go)
+                        break;
+                    uint8_t* dk = smem + slot * 2 * DecCfg::kTileBytes;
+                    uint8_t* dv = dk + DecCfg::kTileBytes;
+                    mbar_arrive_expect_tx(&bar_full[slot], bytes + (t == t0 ? (uint32_t)q_bytes : 0u));
+                    if (t == t0) {
+                        bulk_load(smem + C::kOffQ + (units % q_slots) * q_bytes,
+                                  static_cast<const T*>(p.q) + (size_t)(at.b * p.Hkv + at.hk) * p.R * d_io, (uint32_t)q_bytes,
+                                  &bar_full[slot]);
+                        ++units;
                     }
-                } else {
-                    const bool pre = LIST == kListCat && head_seg;
-                    const CUtensorMap* mk = pre ? &tmK0 : &tmK;
-                    const CUtensorMap* mv = pre ? &tmV0 : &tmV;
-                    const int head = pre ? at.hk : at.b * p.Hkv + at.hk;
-                    for (int pn = 0; pn < (two ? 2 : 1); ++pn) {
-                        tma_load_3d(dk + pn * DecCfg::kPanelBytes, mk, &bar_full[slot], pn * 64, key0, head);
-                        tma_load_3d(dv + pn * DecCfg::kPanelBytes, mv, &bar_full[slot], pn * 64, key0, head);
+                    const bool head_seg = t < at.l.seg;
+                    const int key0 = head_seg ? t * kt : at.l.base + (t - at.l.seg) * kt;
+                    if constexpr (LIST == kListPaged) {
+                        // an out-of-range page id reads zeros (TMA bounds), never another buffer
+                        const int page = __ldg(p.block_table + (size_t)at.b * p.max_pages + key0 / p.page_size);
+                        const int off = key0 % p.page_size;
+                        for (int pn = 0; pn < (two ? 2 : 1); ++pn) {
+                            tma_load_4d(dk + pn * DecCfg::kPanelBytes, &tmK, &bar_full[slot], pn * 64, at.hk, off, page);
+                            tma_load_4d(dv + pn * DecCfg::kPanelBytes, &tmV, &bar_full[slot], pn * 64, at.hk, off, page);
+                        }
+                    } else {
+                        const bool pre = LIST == kListCat && head_seg;
+                        const CUtensorMap* mk = pre ? &tmK0 : &tmK;
+                        const CUtensorMap* mv = pre ? &tmV0 : &tmV;
+                        const int head = pre ? at.hk : at.b * p.Hkv + at.hk;
+                        for (int pn = 0; pn < (two ? 2 : 1); ++pn) {
+                            tma_load_3d(dk + pn * DecCfg::kPanelBytes, mk, &bar_full[slot], pn * 64, key0, head);
+                            tma_load_3d(dv + pn * DecCfg::kPanelBytes, mv, &bar_full[slot], pn * 64, key0, head);
+                        }
                     }
                 }
-                if (++at.t == at.l.tiles && left > 1)
-                    at.next_unit(p);
+                go = go && at.next(p);
             }
             if (*abort_flag)   // let the loads in flight land before the block exits
                 for (int i = max(0, n - C::kStages); i < n; ++i)
@@ -286,12 +330,15 @@ __global__ void __launch_bounds__(160, 2)
     float* sm_o = reinterpret_cast<float*>(smem + C::kOffMerge);   // [4 warps][kMergeRows][128]
     float* sm_m = reinterpret_cast<float*>(smem + C::kOffML);      // [4][16]
     float* sm_l = sm_m + 64;
-    int n = 0;   // tiles taken so far
+    int n = 0, units = 0;   // tiles and units taken so far
     bool ok = true;
-    while (left > 0) {
-        const int unit = at.b * p.Hkv + at.hk, t_first = at.t;
-        const int n_tiles = min(left, at.l.tiles - at.t);
-        // the unit's query rows: row r is head hk * G + r / Nq, query r % Nq, and row r of its R
+    for (bool go = any; go; go = at.next(p)) {
+        const int unit = at.b * p.Hkv + at.hk, t_first = at.off, t_end = at.end();
+        if (t_first >= t_end)   // only places behind the unit's tiles
+            continue;
+        // the unit's query rows (row r is head hk * G + r / Nq, query r % Nq), landed with its first tile
+        ok = mbar_wait(&bar_full[n % C::kStages], (uint32_t)(n / C::kStages) & 1u, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
         uint32_t qa[8][4];
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
@@ -300,12 +347,15 @@ __global__ void __launch_bounds__(160, 2)
                 const int r = g + 8 * hr;
                 qa[ks][hr] = qa[ks][hr + 2] = 0u;
                 if (r < p.R && ks * 16 < d_io) {
-                    const uint32_t* qrow = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) +
-                                                                             ((size_t)unit * p.R + r) * d_io);
-                    qa[ks][hr] = __ldg(qrow + ks * 8 + tq);          // cols 16 ks + 2 tq, + 1
-                    qa[ks][hr + 2] = __ldg(qrow + ks * 8 + 4 + tq);  // cols 16 ks + 8 + 2 tq, + 1
+                    const uint32_t* qrow = reinterpret_cast<const uint32_t*>(smem + C::kOffQ + (units % q_slots) * q_bytes) + r * (d_io / 2);
+                    qa[ks][hr] = qrow[ks * 8 + tq];          // cols 16 ks + 2 tq, + 1
+                    qa[ks][hr + 2] = qrow[ks * 8 + 4 + tq];  // cols 16 ks + 8 + 2 tq, + 1
                 }
             }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&bar_qfree[units % q_slots]);
+        ++units;
         // last visible key of the thread's two rows (own keys), of the prefix, and first window key
         int lim[2], low[2], pre[2];
 #pragma unroll
@@ -321,7 +371,7 @@ __global__ void __launch_bounds__(160, 2)
             o[nd][0] = o[nd][1] = o[nd][2] = o[nd][3] = 0.f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-        for (int i = 0; i < n_tiles; ++i, ++n, ++at.t) {
+        for (int t = t_first; ok && t < t_end; ++t, ++n) {
             const int slot = n % C::kStages;
             ok = mbar_wait(&bar_full[slot], (uint32_t)(n / C::kStages) & 1u, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
@@ -330,8 +380,8 @@ __global__ void __launch_bounds__(160, 2)
             uint8_t* tile = smem + slot * 2 * DecCfg::kTileBytes;
             const uint32_t kbase = smem_u32(tile), vbase = kbase + DecCfg::kTileBytes;
             const int key_w = warp * 16;   // this warp's 16 keys within the tile
-            const bool head_seg = at.t < at.l.seg;
-            const int key0 = (head_seg ? at.t * kt : at.l.base + (at.t - at.l.seg) * kt) + key_w;
+            const bool head_seg = t < at.l.seg;
+            const int key0 = (head_seg ? t * kt : at.l.base + (t - at.l.seg) * kt) + key_w;
 
             // S (16 rows x 16 keys) = Q K^T
             float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -359,20 +409,23 @@ __global__ void __launch_bounds__(160, 2)
                     if (out)
                         s[nt][e] = -INFINITY;
                 }
-            // V rows of keys that no row sees (between the sinks and the window; past the sequence, in
-            // its last page or in the padding) are zeroed: whatever they hold, 0 * V adds nothing
+            // V of keys that no row sees (between the sinks and the window; past the sequence, in its
+            // last page or in the padding) is cleared in the operand registers: whatever is there,
+            // 0 * V adds nothing.  A thread's operand words hold keys 2 tq, 2 tq + 1 (keep[0]) and 8
+            // further on (keep[1]) of the warp's 16.
+            uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+            bool clear = false;
             if (!in_prefix) {
                 constexpr bool kWin = LIST == kListWindow || LIST == kListPaged;
                 const int len = at.l.len, win_lo = at.l.win_lo;
-                if (key0 + 16 > len || (kWin && key0 < win_lo && key0 + 16 > p.sinks)) {
-                    for (int j = lane; j < 256; j += 32) {
-                        const int key = key0 + (j >> 4);
+                clear = key0 + 16 > len || (kWin && key0 < win_lo && key0 + 16 > p.sinks);
+                if (clear) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + 8 * (e >> 1) + 2 * tq + (e & 1);
                         if (key >= len || (kWin && key >= p.sinks && key < win_lo))
-                            *reinterpret_cast<uint4*>(tile + DecCfg::kTileBytes + dec_tile_off(key_w + (j >> 4), j & 15)) =
-                                make_uint4(0u, 0u, 0u, 0u);
+                            keep[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
                     }
-                    fence_proxy_async_smem();   // before the slot is given back to the TMA
-                    __syncwarp();
                 }
             }
             if constexpr (SCORES) {
@@ -417,6 +470,12 @@ __global__ void __launch_bounds__(160, 2)
                         break;
                     uint32_t b0, b1, b2, b3;
                     ldsm_x4_t(vbase + dec_tile_off(key, nd + (mi >> 1)), b0, b1, b2, b3);
+                    if (clear) {
+                        b0 &= keep[0];
+                        b1 &= keep[1];
+                        b2 &= keep[0];
+                        b3 &= keep[1];
+                    }
                     mma_16816<T>(o[nd], pa, b0, b1);
                     mma_16816<T>(o[nd + 1], pa, b2, b3);
                 }
@@ -439,8 +498,7 @@ __global__ void __launch_bounds__(160, 2)
                 sm_l[warp * 16 + g + 8 * hr] = lt;
             }
         }
-        const bool whole = t_first == 0 && at.t == at.l.tiles;
-        const int dcol = threadIdx.x;   // 0..127
+        const bool whole = t_first == 0 && t_end == at.l.tiles;
         for (int r0 = 0; r0 < p.R; r0 += C::kMergeRows) {
             if (r0 > 0)
                 named_bar_sync(1, 128);   // the rows before are read out
@@ -453,60 +511,65 @@ __global__ void __launch_bounds__(160, 2)
                         *reinterpret_cast<float2*>(dst + nd * 8) = make_float2(o[nd][2 * hr], o[nd][2 * hr + 1]);
                 }
             named_bar_sync(1, 128);
-            for (int r = r0; r < min(p.R, r0 + C::kMergeRows); ++r) {
-                float M = -INFINITY;
+            // a row per warp, four columns per lane
+            const int r = r0 + warp, col = lane * 4;
+            if (r >= p.R)
+                continue;
+            float M = -INFINITY, L = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    M = fmaxf(M, sm_m[w * 16 + r]);
-                float L = 0.f, acc = 0.f;
-                if (M != -INFINITY) {
+            for (int w = 0; w < 4; ++w)
+                M = fmaxf(M, sm_m[w * 16 + r]);
+            const float base = M == -INFINITY ? 0.f : M;   // a row without keys: l = 0, o = 0
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const float sc = ex2_approx(sm_m[w * 16 + r] - M);
-                        L += sm_l[w * 16 + r] * sc;
-                        acc += sm_o[(w * C::kMergeRows + r - r0) * 128 + dcol] * sc;
-                    }
-                }
-                const float on = (L > 0.f) ? acc / L : 0.f;
-                const float lse = (L > 0.f) ? M + __log2f(L) : -INFINITY;
-                if (whole && !p.partial) {
-                    const size_t row = (size_t)unit * p.R + r;
-                    if (dcol < d_io)
-                        static_cast<T*>(p.o)[row * d_io + dcol] = Elt<T>::from_float(on);
-                    if (dcol == 0 && p.lse)
-                        p.lse[row] = lse * 0.69314718055994530942f;
-                } else {
-                    const size_t slot = whole ? 2 * (size_t)grid + unit : 2 * (size_t)cta + (t_first == 0 ? 1 : 0);
-                    p.part_o[(slot * p.R + r) * 128 + dcol] = on;
-                    if (dcol == 0)
-                        p.part_lse[slot * p.R + r] = lse;
-                }
+            for (int w = 0; w < 4; ++w) {
+                const float sc = ex2_approx(sm_m[w * 16 + r] - base);
+                const float4 x = *reinterpret_cast<const float4*>(sm_o + (w * C::kMergeRows + warp) * 128 + col);
+                L = fmaf(sm_l[w * 16 + r], sc, L);
+                acc.x = fmaf(x.x, sc, acc.x);
+                acc.y = fmaf(x.y, sc, acc.y);
+                acc.z = fmaf(x.z, sc, acc.z);
+                acc.w = fmaf(x.w, sc, acc.w);
+            }
+            const float inv = (L > 0.f) ? __frcp_rn(L) : 0.f;
+            const float lse = (L > 0.f) ? M + __log2f(L) : -INFINITY;
+            if (whole && !p.partial) {
+                const size_t row = (size_t)unit * p.R + r;
+                if (col < d_io)
+                    *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + row * d_io + col) =
+                        make_uint2(Elt<T>::pack(acc.x * inv, acc.y * inv), Elt<T>::pack(acc.z * inv, acc.w * inv));
+                if (lane == 0 && p.lse)
+                    p.lse[row] = lse * 0.69314718055994530942f;
+            } else {
+                const size_t slot = whole ? 2 * (size_t)grid + unit : 2 * (size_t)cta + (t_first == 0 ? 1 : 0);
+                *reinterpret_cast<float4*>(p.part_o + (slot * p.R + r) * 128 + col) =
+                    make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+                if (lane == 0)
+                    p.part_lse[slot * p.R + r] = lse;
             }
         }
-        left -= n_tiles;
-        if (left > 0)
-            at.next_unit(p);
     }
     if (p.after)
         griddep_wait();
 }
 
-// The parts of a unit that the pass has left: `n` of them, part i in slot slot(i).
+// The parts of a unit that the pass has left.
 struct StreamParts {
     const float* o;       // [slots][R][128]
     const float* lse;     // [slots][R], log2 units
     const int* first;     // [B + 1] or nullptr (tiles each)
-    int tiles, B, Hkv, R, grid, partial;
+    int tiles, B, Hkv, R, grid;   // tiles: of each unit (without lengths)
+    // number of parts, and the CTA of the first; part i is in slot(unit, c0, n, i)
     __device__ __forceinline__ int count(int unit, int& c0) const
     {
-        long long base, n, total;
+        long long base, n, total;   // in places
         if (first) {
             const int b = unit / Hkv, f = first[b];
             n = first[b + 1] - f;
             base = (long long)f * Hkv + (unit % Hkv) * n;
             total = (long long)first[B] * Hkv;
         } else {
-            n = tiles;
+            n = stream_places(tiles);
             base = (long long)unit * n;
             total = (long long)B * Hkv * n;
         }
@@ -514,7 +577,7 @@ struct StreamParts {
         if (n == 0)
             return 0;
         c0 = stream_cta(base, total, grid);
-        return stream_cta(base + n - 1, total, grid) - c0 + 1;
+        return stream_cta(base + n - kUnitPlaces - 1, total, grid) - c0 + 1;   // up to its last tile
     }
     __device__ __forceinline__ size_t slot(int unit, int c0, int n, int i) const
     {
@@ -522,48 +585,87 @@ struct StreamParts {
     }
 };
 
+// Adds up to eight parts' rows at a time, their loads in flight together: part i has its row at
+// row_of(i) (of both o and lse), lane l columns 4 l .. 4 l + 3.  Returns the running (M, L, acc).
+struct MergeState {
+    float M, L;
+    float4 acc;
+};
+
+template <typename F>
+__device__ __forceinline__ void merge_parts(MergeState& st, const float* o, const float* lse, int ld, int n, bool cols, F row_of)
+{
+    const int lane = lane_id();
+    for (int i0 = 0; i0 < n; i0 += 8) {
+        float ls[8];
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            ls[k] = -INFINITY;
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + k < n) {
+                const size_t at = row_of(i0 + k);
+                ls[k] = lse[at];
+                if (cols)
+                    v[k] = *reinterpret_cast<const float4*>(o + at * ld + lane * 4);
+            }
+        }
+        float M = st.M;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            M = fmaxf(M, ls[k]);
+        if (M == -INFINITY)
+            continue;
+        const float a = ex2_approx(st.M - M);
+        st.M = M;
+        st.L *= a;
+        st.acc.x *= a;
+        st.acc.y *= a;
+        st.acc.z *= a;
+        st.acc.w *= a;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (ls[k] == -INFINITY)   // no key there: its row may never have been written
+                continue;
+            const float w = ex2_approx(ls[k] - M);
+            st.L += w;
+            st.acc.x = fmaf(w, v[k].x, st.acc.x);
+            st.acc.y = fmaf(w, v[k].y, st.acc.y);
+            st.acc.z = fmaf(w, v[k].z, st.acc.z);
+            st.acc.w = fmaf(w, v[k].w, st.acc.w);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void merge_store(const MergeState& st, T* o, float* lse, size_t row, int d_io, int col)
+{
+    const float inv = (st.L > 0.f) ? 1.f / st.L : 0.f;
+    if (col < d_io)
+        *reinterpret_cast<uint2*>(o + row * d_io + col) = make_uint2(Elt<T>::pack(st.acc.x * inv, st.acc.y * inv),
+                                                                    Elt<T>::pack(st.acc.z * inv, st.acc.w * inv));
+    if (col == 0 && lse)
+        lse[row] = (st.L > 0.f) ? (st.M + __log2f(st.L)) * 0.69314718055994530942f : -INFINITY;
+}
+
 // One warp per row: the parts of units cut between CTAs; rows of units within one CTA are final,
 // and rows of a sequence without keys get O = 0, LSE = -inf.
 template <typename T>
 __global__ void __launch_bounds__(128) stream_combine_kernel(StreamParts p, void* o_out, float* lse_out, int d_io)
 {
     griddep_launch_dependents();
-    griddep_wait();
     const int row = (int)(blockIdx.x * 4 + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    const int unit = row / p.R, r = row % p.R;
+    griddep_wait();
     if (row >= p.B * p.Hkv * p.R)
         return;
-    const int unit = row / p.R, r = row % p.R;
     int c0;
     const int n = p.count(unit, c0);
     if (n == 1)
         return;
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32)
-        M = fmaxf(M, p.lse[p.slot(unit, c0, n, i) * p.R + r]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
-    if (M != -INFINITY) {
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const size_t at = p.slot(unit, c0, n, i) * p.R + r;
-            const float w = ex2_approx(p.lse[at] - M);
-            const float4 v = *reinterpret_cast<const float4*>(p.o + at * 128 + lane * 4);
-            L += w;
-            acc.x = fmaf(w, v.x, acc.x);
-            acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z);
-            acc.w = fmaf(w, v.w, acc.w);
-        }
-    }
-    const float inv = (L > 0.f) ? 1.f / L : 0.f;
-    if (lane * 4 < d_io)
-        *reinterpret_cast<uint2*>(static_cast<T*>(o_out) + (size_t)row * d_io + lane * 4) =
-            make_uint2(Elt<T>::pack(acc.x * inv, acc.y * inv), Elt<T>::pack(acc.z * inv, acc.w * inv));
-    if (lane == 0 && lse_out)
-        lse_out[row] = (L > 0.f) ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
+    MergeState st{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    merge_parts(st, p.o, p.lse, 128, n, lane * 4 < d_io, [&](int i) { return p.slot(unit, c0, n, i) * p.R + r; });
+    merge_store(st, static_cast<T*>(o_out), lse_out, (size_t)row, d_io, lane * 4);
 }
 
 // The weights that the keys receive, from the scores that the pass has left and the rows' LSE:

@@ -1060,13 +1060,14 @@ StreamPlan stream_plan(const StreamArgs& a)
     case fa::kListCat: pl.tiles = fa::stream_list<fa::kListCat>(p, a.Nk).tiles; break;
     default: pl.tiles = fa::stream_list<fa::kListAll>(p, a.Nk).tiles; break;
     }
-    const long long units = (long long)a.B * a.Hkv, T = units * pl.tiles, most = 2LL * sm_count();
+    const int places = fa::stream_places(pl.tiles);
+    const long long units = (long long)a.B * a.Hkv, T = units * places, most = 2LL * sm_count();
     if (pl.tiles <= 4 && units <= most)
         pl.grid = (int)units;
     else
-        pl.grid = (int)std::max<long long>(1, std::min(most, T / 2));
+        pl.grid = (int)std::max<long long>(1, std::min(most, units * pl.tiles / 2));
     // of equal lists none is cut where every CTA's part is a number of whole ones
-    const bool whole = !a.lens && T % pl.grid == 0 && (T / pl.grid) % pl.tiles == 0;
+    const bool whole = !a.lens && T % pl.grid == 0 && (T / pl.grid) % places == 0;
     pl.merge = !whole;
     const size_t slots = a.partial || pl.merge ? 2 * (size_t)pl.grid + (a.partial ? (size_t)units : 0) : 0;
     pl.lse_off = align256(slots * p.R * kDecodeWidth * 4);
@@ -1087,7 +1088,6 @@ fa::StreamParts stream_parts(const StreamArgs& a, const StreamPlan& pl, void* ws
     q.Hkv = a.Hkv;
     q.R = a.Hq / a.Hkv * a.Nq;
     q.grid = pl.grid;
-    q.partial = a.partial;
     return q;
 }
 
@@ -1177,6 +1177,8 @@ fa_status_t run_stream(const StreamArgs& a, void* workspace, size_t workspace_by
 // ---------------------------------------------------------------------------
 // forward of a batch whose sequences share a prefix
 // ---------------------------------------------------------------------------
+constexpr long long kPrefixUnpackedTiles = 4096;
+
 struct PrefixArgs {
     const void *q, *kp, *vp, *k, *v;
     const int* lens;
@@ -1189,8 +1191,15 @@ struct PrefixArgs {
 
 // Rows of several sequences fit a 128-row tile: the prefix in a pass of its own, which reads it
 // once for all of them, and a merge.  Where a sequence's rows fill half a tile or more, packing
-// saves nothing, and one launch reads the prefix and then the own keys.
-bool prefix_packs(const PrefixArgs& a) { return a.B > 1 && 2LL * (a.Hq / a.Hkv) * a.Nq <= 128; }
+// saves nothing, and one launch reads the prefix and then the own keys.  So it does for a batch and
+// prefix so small that reading the prefix once per sequence (from L2, in the split-KV pass) is
+// quicker than a pass and a merge more: up to 4096 tiles of 64 keys.
+bool prefix_packs(const PrefixArgs& a)
+{
+    if (a.B == 1 || 2LL * (a.Hq / a.Hkv) * a.Nq > 128)
+        return false;
+    return !decode_shape(a.Hq, a.Hkv, a.Nq, a.d) || (long long)a.B * a.Hkv * ((a.Np + 63) / 64) > kPrefixUnpackedTiles;
+}
 
 // 4-D map over q as [B][Hkv][rows][d], box {64, rows, 1, pack}: a kv head's rows of `pack` sequences
 fa_status_t make_map_pack(CUtensorMap* m, const void* base, uint64_t d, uint64_t rows, uint64_t Hkv, uint64_t B,
@@ -1395,7 +1404,7 @@ fa_status_t launch_prefix(const PrefixArgs& a, const PrefixPlan& pl, void* ws, c
     m.rows = (long long)a.B * a.Hq * a.Nq;
     m.o = a.o;
     m.lse = a.lse;
-    return launch_dependent("prefix_merge_kernel launch", fa::prefix_merge_kernel<T>, dim3((unsigned)((m.rows + 3) / 4)),
+    return launch_dependent("prefix_merge_kernel launch", fa::prefix_merge_kernel<T>, dim3((unsigned)((m.rows * ((a.d + 127) / 128) + 3) / 4)),
                             dim3(128), 0, stream, m);
 }
 
