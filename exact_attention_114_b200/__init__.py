@@ -401,6 +401,18 @@ def fa_bwd(q, k, v, o, dout, lse, dq=None, dk=None, dv=None, *, causal=False, sc
 
 
 _NO_CONTEXT = contextlib.nullcontext()
+_CODES = {}   # 16-bit torch dtype -> FA_DTYPE_*; filled with the first call, which imports torch
+
+
+def _code_of(dtype):
+    code = _CODES.get(dtype)
+    if code is None:
+        import torch
+        _CODES.update({torch.bfloat16: FA_DTYPE_BF16, torch.float16: FA_DTYPE_FP16})
+        code = _CODES.get(dtype)
+        if code is None:
+            raise ValueError(f"unsupported dtype {dtype} (bf16 or fp16)")
+    return code
 
 
 def _on_device(stream, dev):
@@ -456,10 +468,12 @@ def _scale(scale, d):
 
 def _qkv(q, k, v):
     """Device, dtype code, sizes and pointers of q, k and v."""
-    B, Hq, Hkv, Nq, Nk, d = _dims(q, k)
-    code, dev, dt = _dtype_code(q), _leader(q, "q"), q.dtype
-    ptrs = (_expect(q, "q", dev, dt), _expect(k, "k", dev, dt), _expect(v, "v", dev, dt, k.shape))
-    return dev, code, (B, Hq, Hkv, Nq, Nk, d), ptrs
+    sq, sk, dt = q.shape, k.shape, q.dtype
+    if len(sq) != 4 or len(sk) != 4 or sq[0] != sk[0] or sq[3] != sk[3]:
+        raise ValueError(f"q {tuple(sq)} and k {tuple(sk)} disagree")
+    code, dev = _code_of(dt), _leader(q, "q")
+    ptrs = (_expect(q, "q", dev, dt), _expect(k, "k", dev, dt), _expect(v, "v", dev, dt, sk))
+    return dev, code, (sq[0], sq[1], sk[1], sq[2], sk[2], sq[3]), ptrs
 
 
 def _new_lse(q):
@@ -528,7 +542,7 @@ def fa_fwd_paged_window(q, k_cache, v_cache, block_table, seq_lens, window, sink
     import torch
     B, Hq, Nq, d = q.shape
     num_pages, page_size, Hkv, dk = k_cache.shape
-    code, dev, dt = _dtype_code(q), _leader(q, "q"), q.dtype
+    code, dev, dt = _code_of(q.dtype), _leader(q, "q"), q.dtype
     if dk != d or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache / v_cache shapes disagree with q")
     if block_table.dim() != 2 or block_table.shape[0] != B:
@@ -585,7 +599,7 @@ def fa_key_weights(q, k, lse, weights=None, weights_out=None, *, causal=False, s
     ``lse`` is that of the forward of the same q, k, scale and causal flag."""
     import torch
     sizes = B, Hq, Hkv, Nq, Nk, d = _dims(q, k)
-    code, dev, f32 = _dtype_code(q), _leader(q, "q"), torch.float32
+    code, dev, f32 = _code_of(q.dtype), _leader(q, "q"), torch.float32
     ptrs = (_expect(q, "q", dev, q.dtype), _expect(k, "k", dev, q.dtype), _expect(lse, "lse", dev, f32, (B, Hq, Nq)),
             _expect(weights, "weights", dev, f32, k.shape[:3]))
     _expect(weights_out, "weights_out", dev, f32, k.shape[:3])
@@ -630,7 +644,7 @@ def fa_kv_evict(k, v, weights, keep, recent=0, seq_lens=None, k_out=None, v_out=
     import torch
     if k.dim() != 4:
         raise ValueError("k must be a contiguous CUDA tensor [B, Hkv, Nk, d]")
-    code, dev, dt, f32 = _dtype_code(k), _leader(k, "k"), k.dtype, torch.float32
+    code, dev, dt, f32 = _code_of(k.dtype), _leader(k, "k"), k.dtype, torch.float32
     B, Hkv, Nk, d = k.shape
     keep, recent = int(keep), int(recent)
     if not 0 <= recent <= keep or keep < 1:

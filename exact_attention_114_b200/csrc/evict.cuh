@@ -307,138 +307,252 @@ __device__ __forceinline__ uint32_t evict_order(float w)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One block per (batch, kv head).  Of its n keys the newest `recent` stay, and of the m before them
-// the `need` = keep - recent heaviest: a radix select finds the need-th largest weight T digit by
-// digit (8 bits each, from the highest), then every warp walks its own contiguous part of the keys:
-// a key stays if it is above T, or equal to T with fewer than the remaining number of equal ones
-// before it.  Its place is the number of kept keys before it, so the kept keys stay in order.
-constexpr int kEvictThreads = 1024;
-constexpr int kEvictCache = 48 * 1024;   // keys whose order numbers are held in shared memory
+// Exclusive prefix sum over the block's threads (1024, in thread order), `warp_sum` [32] in shared memory.
+__device__ __forceinline__ int evict_prefix(int v, int* warp_sum)
+{
+    const int warp = warp_id(), lane = lane_id();
+    int incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off)
+            incl += x;
+    }
+    if (lane == 31)
+        warp_sum[warp] = incl;
+    __syncthreads();
+    int before = lane < warp ? warp_sum[lane] : 0;   // the warps before this one
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+    return before + incl - v;
+}
 
+// One block per (batch, kv head).  Of its n keys the newest `recent` stay, and of the m before them
+// the `need` = keep - recent heaviest.  The need-th largest weight T is found digit by digit from the
+// highest (11, 11 and 10 bits): a histogram of the digit, and the bin in which the count from above
+// reaches what is left.  The first digit takes the sign, the exponent and two bits of the mantissa, so
+// that few keys are left for the next ones; they are listed in shared memory (where they fit).  Then
+// every warp walks its own contiguous part of the keys: a key stays if it is above T, or equal to T
+// with fewer than the remaining number of equal ones before it.  Its place is the number of kept keys
+// before it, so the kept keys stay in order.
+// FUSED: the block also moves the kept rows, where they are few: a launch less (small caches are bound
+// by the launches).
+constexpr int kEvictThreads = 1024;
+constexpr int kEvictCache = 40 * 1024;   // keys whose order numbers are held in shared memory
+constexpr int kEvictList = 8 * 1024;     // keys listed after the first digit
+constexpr int kEvictBins = 2048;
+
+template <bool FUSED>
 __global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(EvictParams p)
 {
-    extern __shared__ uint32_t s_cache[];
-    __shared__ int s_hist[256];
-    __shared__ int s_gt[32], s_eq[32];
+    extern __shared__ uint32_t s_mem[];
+    uint32_t* s_list = s_mem;                 // [kEvictList]
+    uint32_t* s_cache = s_mem + kEvictList;
+    __shared__ int s_hist[kEvictBins];
+    __shared__ int s_warp[32], s_eq[32];
     __shared__ uint32_t s_digit;
-    __shared__ int s_left;
+    __shared__ int s_left, s_listed;
     griddep_launch_dependents();
-    const int row = (int)blockIdx.x, warp = warp_id(), lane = lane_id();
+    const int row = (int)blockIdx.x, tid = (int)threadIdx.x, warp = warp_id(), lane = lane_id();
     const int n = p.seq_lens ? max(0, min(__ldg(p.seq_lens + row / p.Hkv), p.Nk)) : p.Nk;
     const float* w = p.w + (size_t)row * p.Nk;
     int* index = p.index + (size_t)row * p.keep;
     float* w_out = p.w_out ? p.w_out + (size_t)row * p.keep : nullptr;
     if (n <= p.keep) {   // all of them
-        for (int i = (int)threadIdx.x; i < n; i += kEvictThreads) {
+        for (int i = tid; i < n; i += kEvictThreads) {
             index[i] = i;
             if (w_out)
                 w_out[i] = w[i];
         }
-        return;
-    }
-    const int m = n - p.recent;             // recent <= keep < n
-    const int need = p.keep - p.recent;     // < m
-    const bool cached = m <= kEvictCache;
-    if (cached) {
-        for (int i = (int)threadIdx.x; i < m; i += kEvictThreads)
-            s_cache[i] = evict_order(w[i]);
-        __syncthreads();
-    }
-    auto order = [&](int i) { return cached ? s_cache[i] : evict_order(__ldg(w + i)); };
-
-    uint32_t T = 0xFFFFFFFFu;   // need = 0: nothing is above it, and none of the equal ones stays
-    int left = 0;               // how many of the keys equal to T stay
-    if (need > 0) {
-        T = 0;
-        left = need;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = (int)threadIdx.x; i < 256; i += kEvictThreads)
-                s_hist[i] = 0;
-            __syncthreads();
-            const uint32_t above = shift == 24 ? 0u : (0xFFFFFFFFu << (shift + 8));
-            for (int i0 = 0; i0 < m; i0 += kEvictThreads) {
-                const int i = i0 + (int)threadIdx.x;
-                const uint32_t u = i < m ? order(i) : 0u;
-                const bool in = i < m && (u & above) == (T & above);
-                const int digit = in ? (int)((u >> shift) & 255u) : 256;
-                // one addition per distinct digit of a warp (weights share their exponents)
-                const unsigned same = __match_any_sync(0xffffffffu, digit);
-                if (in && lane == __ffs((int)same) - 1)
-                    atomicAdd(&s_hist[digit], __popc(same));
-            }
-            __syncthreads();
-            if (warp == 0) {
-                // bins from the highest down: lane l holds bins 255 - 8 l .. 248 - 8 l
-                int c[8], sum = 0;
-                for (int k = 0; k < 8; ++k) {
-                    c[k] = s_hist[255 - 8 * lane - k];
-                    sum += c[k];
-                }
-                int before = sum;
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int x = __shfl_up_sync(0xffffffffu, before, off);
-                    if (lane >= off)
-                        before += x;
-                }
-                before -= sum;   // keys in higher bins than this lane's
-                if (before < left && left <= before + sum) {
-                    int rest = left - before;
-                    int k = 0;
-                    while (rest > c[k])
-                        rest -= c[k++];
-                    s_digit = (uint32_t)(255 - 8 * lane - k);
-                    s_left = rest;
-                }
-            }
-            __syncthreads();
-            T |= s_digit << shift;
-            left = s_left;
-            __syncthreads();
-        }
-    }
-    // counts above and at T in each warp's part
-    const int part = (m + 31) / 32, lo = min(m, warp * part), hi = min(m, lo + part);
-    int gt = 0, eq = 0;
-    for (int i = lo + lane; i < hi; i += 32) {
-        const uint32_t u = order(i);
-        gt += u > T;
-        eq += u == T;
-    }
+    } else {
+        const int m = n - p.recent;             // recent <= keep < n
+        const int need = p.keep - p.recent;     // < m
+        const bool cached = m <= kEvictCache;
+        // eight keys' order numbers, `step` apart, their loads in flight together (0 past `end`)
+        constexpr int kAtOnce = 8;
+        auto orders = [&](uint32_t (&u)[kAtOnce], int i, int step, int end) {
+            if (cached) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        gt += __shfl_xor_sync(0xffffffffu, gt, off);
-        eq += __shfl_xor_sync(0xffffffffu, eq, off);
-    }
-    if (lane == 0) {
-        s_gt[warp] = gt;
-        s_eq[warp] = eq;
-    }
-    __syncthreads();
-    gt = eq = 0;
-    for (int i = 0; i < warp; ++i) {
-        gt += s_gt[i];
-        eq += s_eq[i];
-    }
-    const unsigned below = (1u << lane) - 1u;
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t u = i < hi ? order(i) : 0u;
-        const bool is_gt = i < hi && u > T, is_eq = i < hi && u == T;
-        const unsigned bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
-        const int eq_before = eq + __popc(be & below);
-        if (is_gt || (is_eq && eq_before < left)) {
-            const int at = gt + __popc(bg & below) + min(eq_before, left);
-            index[at] = i;
-            if (w_out)
-                w_out[at] = w[i];
+                for (int k = 0; k < kAtOnce; ++k)
+                    u[k] = i + k * step < end ? s_cache[i + k * step] : 0u;
+            } else {
+                float x[kAtOnce];
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k)
+                    x[k] = i + k * step < end ? __ldg(w + i + k * step) : 0.f;
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k)
+                    u[k] = evict_order(x[k]);
+            }
+        };
+        uint32_t T = 0xFFFFFFFFu;   // need = 0: nothing is above it, and none of the equal ones stays
+        int left = 0;               // how many of the keys equal to T stay
+        // count one key's digit: one addition where a warp's keys agree (equal weights)
+        auto count = [&](bool in, int digit) {
+            const unsigned who = __ballot_sync(0xffffffffu, in);
+            int same;
+            __match_all_sync(0xffffffffu, in ? digit : -1, &same);
+            if (same) {
+                if (in && lane == 0)
+                    atomicAdd(&s_hist[digit], __popc(who));
+            } else if (in) {
+                atomicAdd(&s_hist[digit], 1);
+            }
+        };
+        // the bin, from the highest, in which `left` keys are reached; two bins per thread
+        auto find = [&]() {
+            __syncthreads();
+            const int hi = kEvictBins - 1 - 2 * tid, a = s_hist[hi], b = s_hist[hi - 1];
+            const int before = evict_prefix(a + b, s_warp);
+            if (before < left && left <= before + a) {
+                s_digit = (uint32_t)hi;
+                s_left = left - before;
+            } else if (before + a < left && left <= before + a + b) {
+                s_digit = (uint32_t)(hi - 1);
+                s_left = left - before - a;
+            }
+            __syncthreads();
+            left = s_left;
+            return s_digit;
+        };
+        auto clear = [&]() {
+            s_hist[tid] = 0;
+            s_hist[tid + kEvictThreads] = 0;
+            __syncthreads();
+        };
+        static_assert(kEvictBins == 2 * kEvictThreads, "two bins per thread");
+        if (tid == 0)
+            s_listed = 0;
+        clear();
+        if (need > 0 || cached) {
+            for (int i0 = 0; i0 < m; i0 += kAtOnce * kEvictThreads) {
+                float x[kAtOnce];
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const int i = i0 + k * kEvictThreads + tid;
+                    x[k] = i < m ? __ldg(w + i) : 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const int i = i0 + k * kEvictThreads + tid;
+                    if (i0 + k * kEvictThreads >= m)
+                        break;
+                    const uint32_t u = evict_order(x[k]);
+                    if (cached && i < m)
+                        s_cache[i] = u;
+                    count(i < m, (int)(u >> 21));
+                }
+            }
         }
-        gt += __popc(bg);
-        eq += __popc(be);
+        if (need > 0) {
+            left = need;
+            T = find() << 21;
+            const int in_bin = s_hist[T >> 21];
+            const bool listed = in_bin <= kEvictList;
+            if (listed) {
+                for (int i0 = 0; i0 < m; i0 += kAtOnce * kEvictThreads) {
+                    uint32_t u[kAtOnce];
+                    orders(u, i0 + tid, kEvictThreads, m);
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k)
+                        if (i0 + k * kEvictThreads + tid < m && (u[k] >> 21) == (T >> 21))
+                            s_list[atomicAdd(&s_listed, 1)] = u[k];
+                }
+                __syncthreads();
+            }
+            const int c = listed ? in_bin : m;   // keys that the next digits look at
+            for (int d = 0; d < 2; ++d) {
+                const int shift = d == 0 ? 10 : 0, above = d == 0 ? 21 : 10;
+                clear();
+                const uint32_t digits = d == 0 ? 2047u : 1023u;
+                if (listed) {
+                    for (int i0 = 0; i0 < c; i0 += kEvictThreads) {
+                        const int i = i0 + tid;
+                        const uint32_t u = i < c ? s_list[i] : 0u;
+                        count(i < c && (u >> above) == (T >> above), (int)((u >> shift) & digits));
+                    }
+                } else {
+                    for (int i0 = 0; i0 < c; i0 += kAtOnce * kEvictThreads) {
+                        uint32_t u[kAtOnce];
+                        orders(u, i0 + tid, kEvictThreads, c);
+#pragma unroll
+                        for (int k = 0; k < kAtOnce; ++k)
+                            count(i0 + k * kEvictThreads + tid < c && (u[k] >> above) == (T >> above),
+                                  (int)((u[k] >> shift) & digits));
+                    }
+                }
+                T |= find() << shift;
+            }
+        }
+        // counts above and at T in each warp's part
+        const int part = ((m + 31) / 32 + 31) / 32 * 32, lo = min(m, warp * part), hi = min(m, lo + part);
+        int gt = 0, eq = 0;
+        __syncthreads();
+        for (int i0 = lo; i0 < hi; i0 += 32 * kAtOnce) {
+            uint32_t u[kAtOnce];
+            orders(u, i0 + lane, 32, hi);
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const bool in = i0 + 32 * k + lane < hi;
+                gt += in && u[k] > T;
+                eq += in && u[k] == T;
+            }
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            gt += __shfl_xor_sync(0xffffffffu, gt, off);
+            eq += __shfl_xor_sync(0xffffffffu, eq, off);
+        }
+        if (lane == 0) {
+            s_warp[warp] = gt;
+            s_eq[warp] = eq;
+        }
+        __syncthreads();
+        gt = lane < warp ? s_warp[lane] : 0;
+        eq = lane < warp ? s_eq[lane] : 0;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            gt += __shfl_xor_sync(0xffffffffu, gt, off);
+            eq += __shfl_xor_sync(0xffffffffu, eq, off);
+        }
+        const unsigned below = (1u << lane) - 1u;
+        for (int i0 = lo; i0 < hi; i0 += 32 * kAtOnce) {
+            uint32_t u[kAtOnce];
+            orders(u, i0 + lane, 32, hi);
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int i = i0 + 32 * k + lane;
+                const bool is_gt = i < hi && u[k] > T, is_eq = i < hi && u[k] == T;
+                const unsigned bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
+                const int eq_before = eq + __popc(be & below);
+                if (is_gt || (is_eq && eq_before < left)) {
+                    const int at = gt + __popc(bg & below) + min(eq_before, left);
+                    index[at] = i;
+                    if (w_out)
+                        w_out[at] = w[i];
+                }
+                gt += __popc(bg);
+                eq += __popc(be);
+            }
+        }
+        for (int i = m + tid; i < n; i += kEvictThreads) {
+            index[need + i - m] = i;
+            if (w_out)
+                w_out[need + i - m] = w[i];
+        }
     }
-    for (int i = m + (int)threadIdx.x; i < n; i += kEvictThreads) {
-        index[need + i - m] = i;
-        if (w_out)
-            w_out[need + i - m] = w[i];
+    if constexpr (FUSED) {
+        __syncthreads();   // the indices, written by this block
+        const int moved = min(n, p.keep) * p.chunks;
+        const size_t in = (size_t)row * p.Nk * p.chunks, out = (size_t)row * p.keep * p.chunks;
+        for (int c = tid; c < moved; c += kEvictThreads) {
+            const int j = c / p.chunks;
+            const size_t from = in + (size_t)index[j] * p.chunks + (c - j * p.chunks);
+            const uint4 a = p.k[from], b = p.v[from];
+            p.k_out[out + c] = a;
+            p.v_out[out + c] = b;
+        }
     }
 }
 

@@ -1708,6 +1708,9 @@ fa_status_t check_weights(const float* in, const float* out, size_t n)
     return FA_OK;
 }
 
+// Kept rows of K and V of a (batch, kv head) up to which the selecting block moves them itself.
+constexpr size_t kEvictFusedBytes = 128 * 1024;
+
 // ---------------------------------------------------------------------------
 // timeout self-test
 // ---------------------------------------------------------------------------
@@ -2506,13 +2509,15 @@ fa_status_t fa_kv_evict(fa_dtype_t dtype, const void* k, const void* v, const fl
     p.chunks = d / 8;
     p.keep = keep;
     p.recent = recent;
-    const int cache = std::min(Nk, fa::kEvictCache) * 4;
-    st = ensure_smem(reinterpret_cast<const void*>(&fa::evict_select_kernel), fa::kEvictCache * 4);
+    const int cache = (std::min(Nk, fa::kEvictCache) + fa::kEvictList) * 4;
+    const bool fused = (size_t)keep * d * 4 <= kEvictFusedBytes;
+    auto select = fused ? fa::evict_select_kernel<true> : fa::evict_select_kernel<false>;
+    st = ensure_smem(reinterpret_cast<const void*>(select), (fa::kEvictCache + fa::kEvictList) * 4);
     if (st == FA_OK) {
-        fa::evict_select_kernel<<<(unsigned)BH, fa::kEvictThreads, cache, s>>>(p);
+        select<<<(unsigned)BH, fa::kEvictThreads, cache, s>>>(p);
         st = check_launch("evict_select_kernel launch");
     }
-    if (st == FA_OK) {
+    if (st == FA_OK && !fused) {
         const size_t per = ((size_t)keep * p.chunks + 256 * fa::kGatherItems - 1) / (256 * fa::kGatherItems);
         st = launch_dependent("evict_gather_kernel launch", fa::evict_gather_kernel, dim3((unsigned)(BH * per)), dim3(256),
                               0, s, p);
