@@ -32,32 +32,58 @@ struct KeyWeightParams {
     float scale_log2;
 };
 
+// 2^x for both lanes on the FMA pipe: x = n + f, f in [-1/2, 1/2], times the degree-5 polynomial
+// through 2^f at the six Chebyshev nodes cos((2 k + 1) pi / 12) / 2 (relative error 2.4e-7; the
+// degree-4 one of the forward has 3.6e-6, which sums of weights in fp32 would show).
+constexpr float kKeyExp2C0 = 1.0000001192092896f, kKeyExp2C1 = 0.69314718246459961f,
+                kKeyExp2C2 = 0.24022106826305389f, kKeyExp2C3 = 0.055503569543361664f,
+                kKeyExp2C4 = 0.009676031768321991f, kKeyExp2C5 = 0.0013390863314270973f;
+
+__device__ __forceinline__ float2 key_weight_exp2(float2 x)
+{
+    x.x = fmaxf(x.x, -125.f);
+    x.y = fmaxf(x.y, -125.f);
+    const float2 t = fadd2(x, make_float2(12582912.f, 12582912.f));
+    const float2 f = fadd2(x, fadd2(make_float2(12582912.f, 12582912.f), make_float2(-t.x, -t.y)));
+    float2 q = ffma2(make_float2(kKeyExp2C5, kKeyExp2C5), f, make_float2(kKeyExp2C4, kKeyExp2C4));
+    q = ffma2(q, f, make_float2(kKeyExp2C3, kKeyExp2C3));
+    q = ffma2(q, f, make_float2(kKeyExp2C2, kKeyExp2C2));
+    q = ffma2(q, f, make_float2(kKeyExp2C1, kKeyExp2C1));
+    q = ffma2(q, f, make_float2(kKeyExp2C0, kKeyExp2C0));
+    return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(t.x) << 23)),
+                       __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
+}
+
+// pairs in four whose exponentials go to the FMA pipe
+constexpr int kKeyPoly = 1;
+
 template <int D>
 struct KeyWCfg {
-    static constexpr int kThreads = 384;
+    static constexpr int kCtas = D == 256 ? 1 : 2;       // per SM
+    static constexpr int kGroups = 4 / kCtas;            // consumer warpgroups, each with a TMEM buffer
+    static constexpr int kThreads = kGroups * 128 + 64;
     static constexpr int kPanels = D / 64;
     static constexpr int kPanelBytes = 128 * 128;        // 128 rows x 64 elements
     static constexpr int kTileBytes = kPanels * kPanelBytes;
-    static constexpr int kStages = D == 256 ? 2 : D == 128 ? 4 : 6;
+    static constexpr int kStages = D == 64 ? 4 : 2;
     static constexpr int kOffK = 0;
     static constexpr int kOffQ = kTileBytes;
-    static constexpr int kOffVec = kOffQ + kStages * kTileBytes;   // [2 groups][2][128] -LSE log2(e), then positions
-    static constexpr int kOffSum = kOffVec + 2 * 2 * 128 * 8;      // [128] sums of the second group
-    static constexpr int kOffBar = kOffSum + 512;
+    static constexpr int kOffVec = kOffQ + kStages * kTileBytes;   // per group: [2][128] -LSE log2(e), then positions
+    static constexpr int kOffSum = kOffVec + kGroups * 2 * 128 * 8;   // [kGroups][128] sums
+    static constexpr int kOffBar = kOffSum + kGroups * 512;
     static constexpr int kSmemBytes = kOffBar + 256 + 1024;
-    static constexpr uint32_t kRegsSoftmax = 208, kRegsOther = 88;
-    static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "register split");
     static_assert((1 + 2 * kStages + 9) * 8 + 8 <= 256, "barrier area");
-    static_assert(kSmemBytes <= 232448, "shared memory per block");
+    static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory per SM");
 };
 
-// One CTA per (key block of 128, batch and kv head, share of the steps).  A step is 128 query rows:
-// S^T = K Q^T (keys along TMEM lanes) goes to one of four TMEM buffers, and the two consumer
-// warpgroups take the steps in turn: thread r holds key r, so a step's sum over rows is a sum over
+// One CTA per (key block of 128, batch and kv head, share of the steps), two per SM (one at d = 256):
+// one starts or ends while the other computes.  A step is 128 query rows: S^T = K Q^T (keys along TMEM
+// lanes) goes to a TMEM buffer, and the consumer warpgroups take the steps in turn: thread r holds key r, so a step's sum over rows is a sum over
 // the thread's own registers, and no two threads ever add to the same key.  The exponentials bound
-// it (128 x 128 of them against 2 x 128 x 128 x d flops): one pair in four goes to the FMA pipe.
+// it (128 x 128 of them against 2 x 128 x 128 x d flops): one pair in four goes to the FMA pipe, and
+// four warps per scheduler keep both pipes fed across the waits for TMEM and barriers.
 template <int D, typename T>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(KeyWCfg<D>::kThreads, KeyWCfg<D>::kCtas)
     key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        KeyWeightParams p)
 {
@@ -69,12 +95,13 @@ __global__ void __launch_bounds__(384, 1)
     uint64_t* bar_k = reinterpret_cast<uint64_t*>(smem + C::kOffBar);   // K landed
     uint64_t* bar_full = bar_k + 1;                 // [kStages] Q slot landed
     uint64_t* bar_empty = bar_full + C::kStages;    // [kStages] Q slot read
-    uint64_t* bar_s = bar_empty + C::kStages;       // [4] S^T of a step in TMEM
-    uint64_t* bar_free = bar_s + 4;                 // [4] read out (count 4)
+    uint64_t* bar_s = bar_empty + C::kStages;       // [kGroups] S^T of a step in TMEM
+    uint64_t* bar_free = bar_s + 4;                 // [kGroups] read out (count 4)
     uint64_t* bar_drain = bar_free + 4;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
+    constexpr int kTma = C::kGroups * 4, kMma = kTma + 1;   // warps
     const int warp = warp_id(), lane = lane_id();
     const int BH = p.B * p.Hkv;
     // blocks of the first keys, which most rows see, first
@@ -107,7 +134,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&bar_full[s], 1);
             mbar_init(&bar_empty[s], 1);
         }
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < C::kGroups; ++b) {
             mbar_init(&bar_s[b], 1);
             mbar_init(&bar_free[b], 4);
         }
@@ -115,8 +142,8 @@ __global__ void __launch_bounds__(384, 1)
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 9) {
-        tmem_alloc(tmem_slot, 512);
+    if (warp == kMma) {
+        tmem_alloc(tmem_slot, 128 * C::kGroups);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -124,13 +151,12 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp >= 8) {
-        regs_dec<C::kRegsOther>();
-        if (warp == 8 && lane == 0 && n_it > 0) {
+    if (warp >= kTma) {
+        if (warp == kTma && lane == 0 && n_it > 0) {
             // ------------------------------------------------------------ TMA producer
             mbar_arrive_expect_tx(bar_k, C::kTileBytes);
-            for (int pn = 0; pn < C::kPanels; ++pn)
-                tma_load_3d(smem + C::kOffK + pn * C::kPanelBytes, &tmK, bar_k, pn * 64, kb * 128, kvh);
+            for (int i = 0; i < C::kPanels; ++i)
+                tma_load_3d(smem + C::kOffK + i * C::kPanelBytes, &tmK, bar_k, i * 64, kb * 128, kvh);
             int issued = 0;
             for (int it = 0; it < n_it; ++it) {
                 const int s = it % C::kStages;
@@ -150,17 +176,18 @@ __global__ void __launch_bounds__(384, 1)
                 for (int i = max(0, issued - C::kStages); i < issued; ++i)
                     mbar_wait_limited(&bar_full[i % C::kStages], (uint32_t)((i / C::kStages) & 1), FA_WAIT_LIMIT_CYCLES);
             }
-        } else if (warp == 9 && n_it > 0) {
+        } else if (warp == kMma && n_it > 0) {
             // ------------------------------------------------------------ MMA issuer
             const uint32_t id = idesc_f16kind(Elt<T>::kMmaFmt, 128, 128, false, false);
             const uint64_t dK = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
             const uint64_t dQ = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
             bool ok = mbar_wait_w(bar_k, 0, abort_flag);
             for (int it = 0; ok && it < n_it; ++it) {
-                const int s = it % C::kStages, b = it & 3;
+                const int s = it % C::kStages;
                 if (!(ok = mbar_wait_w(&bar_full[s], (uint32_t)((it / C::kStages) & 1), abort_flag)))
                     break;
-                if (!(ok = mbar_wait_w(&bar_free[b], (uint32_t)((it >> 2) & 1) ^ 1u, abort_flag)))
+                const int b = it % C::kGroups;
+                if (!(ok = mbar_wait_w(&bar_free[b], (uint32_t)((it / C::kGroups) & 1) ^ 1u, abort_flag)))
                     break;
                 tc_fence_after();
 #pragma unroll 4
@@ -169,8 +196,8 @@ __global__ void __launch_bounds__(384, 1)
                     mma_ss_w(tmem + 128u * (uint32_t)b, dK + (uint64_t)(o >> 4),
                              dQ + (uint64_t)((o + (uint32_t)(s * C::kTileBytes)) >> 4), id, kk > 0 ? 1u : 0u);
                 }
-                mma_commit_w(&bar_empty[s]);
                 mma_commit_w(&bar_s[b]);
+                mma_commit_w(&bar_empty[s]);
             }
             if (!ok) {
                 mma_commit_w(bar_drain);
@@ -178,10 +205,9 @@ __global__ void __launch_bounds__(384, 1)
             }
         }
     } else {
-        regs_inc<C::kRegsSoftmax>();
         // ------------------------------------------------------------ exponentials and sums
         const int g = warp >> 2, c0 = threadIdx.x & 127;
-        const int r = ((warp & 3) << 5) + lane;            // key within the block = TMEM lane
+        const int r = ((warp & 3) << 5) + lane;            // key within its tile = TMEM lane
         const int key = kb * 128 + r;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         float* vec = reinterpret_cast<float*>(smem + C::kOffVec) + g * 512;   // [2][128] floats, then [2][128] ints
@@ -190,71 +216,101 @@ __global__ void __launch_bounds__(384, 1)
         const float2 sl22 = make_float2(sl2, sl2);
         float sum = 0.f;
         bool ok = true;
-        for (int it = g, u = 0; it < n_it; it += 2, ++u) {
-            int th, row0;
-            step(it, th, row0);
-            // -LSE log2(e) of the step's rows: -inf (P = 0) for rows past the last and rows that see no key
-            const int row = row0 + c0;
-            float nl = -INFINITY;
-            if (row < p.rows) {
-                const float l = __ldg(p.lse + (size_t)th * p.rows + row);
-                nl = (l == -INFINITY) ? -INFINITY : -l * 1.4426950408889634f;
-            }
+        // the group's next step: tile head th, query block qb of its nqb
+        int th = 0, qb = 0;
+        if (n_it > 0) {
+            th = kvh * p.heads + (it_lo + g) / nqb;
+            qb = (it_lo + g) % nqb;
+        }
+        // LSE of this thread's row of the next step (loaded a step ahead); rows past the last count as
+        // seeing no key
+        auto next_lse = [&](int it) {
+            const int row = (qb0 + qb) * 128 + c0;
+            return it < n_it && row < p.rows ? __ldg(p.lse + (size_t)th * p.rows + row) : -INFINITY;
+        };
+        float lse_next = next_lse(g);
+        for (int it = g, u = 0; it < n_it; it += C::kGroups, ++u) {
+            const int row0 = (qb0 + qb) * 128, row = row0 + c0;
+            // -LSE log2(e) of the step's rows: -inf (P = 0) for rows that see no key
+            const float nl = (lse_next == -INFINITY) ? -INFINITY : -lse_next * 1.4426950408889634f;
+            for (qb += C::kGroups; qb >= nqb; qb -= nqb)
+                ++th;
+            lse_next = next_lse(it + C::kGroups);
             float* v = vec + (u & 1) * 128;
             int* ps = pos + (u & 1) * 128;
             v[c0] = nl;
-            ps[c0] = row % p.Nq + delta;
-            named_bar_sync(1 + g, 128);   // also: nobody still reads the buffer of two steps ago
-            const int b = it & 3;
-            ok = mbar_wait(&bar_s[b], (uint32_t)((it >> 2) & 1), abort_flag);
-            ok = named_bar_and(1 + g, 128, ok);   // the four warps go on or stop together
+            if (p.causal)
+                ps[c0] = (p.rows == p.Nq ? row : row % p.Nq) + delta;
+            // (nobody still reads the buffer of two steps ago; the four warps go on or stop together)
+            ok = named_bar_and(1 + g, 128, ok);
             if (!ok)
                 break;
+            const int b = g;
+            ok = mbar_wait(&bar_s[b], (uint32_t)(u & 1), abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                continue;
             tc_fence_after();
-            uint32_t sr[128];
-            tmem_ld128(tmem + lane_off + 128u * (uint32_t)b, sr);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bar_free[b]);
-            const float4* v4 = reinterpret_cast<const float4*>(v);
             // rows whose position does not reach the key: only in the blocks on the diagonal
             // (every block of a run of short groups)
             const bool masked = p.causal && (p.rows != p.Nq || row0 + delta < kb * 128 + 127);
+            const float4* v4 = reinterpret_cast<const float4*>(v);
             float2 a0 = make_float2(0.f, 0.f), a1 = a0;
-            auto sums = [&](auto mask_rows) {
 #pragma unroll
-                for (int c = 0; c < 128; c += 4) {
-                    const float4 n4 = v4[c >> 2];
-                    float2 x0 = ffma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl22,
-                                      make_float2(n4.x, n4.y));
-                    float2 x1 = ffma2(make_float2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl22,
-                                      make_float2(n4.z, n4.w));
-                    if (decltype(mask_rows)::value) {
-                        const int4 p4 = *reinterpret_cast<const int4*>(ps + c);
+            for (int h = 0; h < 4; ++h) {
+                uint32_t sr[32];
+                tmem_ld32(tmem + lane_off + 128u * (uint32_t)b + 32u * h, sr);
+                if (h == 3) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bar_free[b]);
+                }
+                if (!masked) {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 8) {
+                        const float4 n0 = v4[8 * h + (c >> 2)], n1 = v4[8 * h + (c >> 2) + 1];
+                        const float2 x0 = ffma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl22,
+                                                make_float2(n0.x, n0.y));
+                        const float2 x1 = ffma2(make_float2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl22,
+                                                make_float2(n0.z, n0.w));
+                        const float2 x2 = ffma2(make_float2(__uint_as_float(sr[c + 4]), __uint_as_float(sr[c + 5])), sl22,
+                                                make_float2(n1.x, n1.y));
+                        const float2 x3 = ffma2(make_float2(__uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7])), sl22,
+                                                make_float2(n1.z, n1.w));
+                        a0 = fadd2(a0, make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
+                        a1 = fadd2(a1, make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
+                        a0 = fadd2(a0, kKeyPoly >= 2 ? key_weight_exp2(x2) : make_float2(ex2_approx(x2.x), ex2_approx(x2.y)));
+                        a1 = fadd2(a1, kKeyPoly >= 1 ? key_weight_exp2(x3) : make_float2(ex2_approx(x3.x), ex2_approx(x3.y)));
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 n4 = v4[8 * h + (c >> 2)];
+                        const int4 p4 = *reinterpret_cast<const int4*>(ps + 32 * h + c);
+                        float2 x0 = ffma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl22,
+                                          make_float2(n4.x, n4.y));
+                        float2 x1 = ffma2(make_float2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl22,
+                                          make_float2(n4.z, n4.w));
                         x0.x = p4.x >= key ? x0.x : -INFINITY;
                         x0.y = p4.y >= key ? x0.y : -INFINITY;
                         x1.x = p4.z >= key ? x1.x : -INFINITY;
                         x1.y = p4.w >= key ? x1.y : -INFINITY;
+                        a0 = fadd2(a0, make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
+                        a1 = fadd2(a1, make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
                     }
-                    a0 = fadd2(a0, make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
-                    a1 = fadd2(a1, make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
                 }
-            };
-            if (masked)
-                sums(std::true_type{});
-            else
-                sums(std::false_type{});
+            }
             sum += (a0.x + a0.y) + (a1.x + a1.y);
         }
-        // the two groups' sums, in a fixed order
-        float* other = reinterpret_cast<float*>(smem + C::kOffSum);
-        if (g == 1)
-            other[r] = sum;
-        named_bar_sync(3, 256);
+        // the groups' sums, in a fixed order
+        float* sums = reinterpret_cast<float*>(smem + C::kOffSum);
+        sums[g * 128 + r] = sum;
+        named_bar_sync(C::kGroups + 1, C::kGroups * 128);
         if (g == 0 && ok && !*abort_flag && key < p.Nk) {
             const size_t at = (size_t)kvh * p.Nk + key;
-            sum += other[r];
+            for (int k = 1; k < C::kGroups; ++k)
+                sum += sums[k * 128 + r];
             if (p.nsp > 1)
                 p.part[(size_t)sp * BH * p.Nk + at] = sum;
             else
@@ -263,9 +319,9 @@ __global__ void __launch_bounds__(384, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kMma) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, 128 * C::kGroups);
     }
 }
 
