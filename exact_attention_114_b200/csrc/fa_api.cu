@@ -1634,11 +1634,13 @@ fa_status_t launch_key_weights(const void* q, const void* k, fa::KeyWeightParams
     if ((st = make_map(&mk, k, d, p.Nk, BH, 128, tma_type<T>())) != FA_OK) return st;
     auto kern = fa::key_weights_kernel<D, T>;
     if ((st = ensure_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes)) != FA_OK) return st;
-    // Enough CTAs to fill the SMs a few times over, as long as each keeps 16 steps
+    // CTAs for three rounds of the SMs' places (fewer leave a long last one, more start too often:
+    // GQA 32/8, 4096 rows, d = 128 takes 103 us with half of that, 96 with this, 102 with twice), as
+    // long as each keeps 16 steps
     const long long units = (long long)BH * ((p.Nk + 127) / 128), steps = (long long)p.heads * ((p.rows + 127) / 128);
     const int sms = sm_count();
     p.nsp = 1;
-    while (p.nsp < 64 && units * p.nsp < 3LL * sms && steps >= 32LL * p.nsp)
+    while (p.nsp < 64 && units * p.nsp < 3LL * C::kCtas * sms && steps >= 16LL * p.nsp)
         p.nsp *= 2;
     void* ws = nullptr;
     if (p.nsp > 1) {
@@ -1710,6 +1712,21 @@ fa_status_t check_weights(const float* in, const float* out, size_t n)
 
 // Kept rows of K and V of a (batch, kv head) up to which the selecting block moves them itself.
 constexpr size_t kEvictFusedBytes = 128 * 1024;
+
+// No exception (host memory) passes a C entry.
+template <typename F>
+fa_status_t guarded(F&& call) noexcept
+{
+    try {
+        return call();
+    } catch (...) {
+        try {
+            t_error = "out of host memory";
+        } catch (...) {
+        }
+        return FA_ERR_CUDA;
+    }
+}
 
 // ---------------------------------------------------------------------------
 // timeout self-test
@@ -2230,16 +2247,24 @@ fa_status_t fa_bwd_ex(fa_dtype_t dtype, const void* q, const void* k, const void
                      workspace, workspace_bytes, stream);
 }
 
+// Whether a size query's sizes are ones that the call would take (no error is recorded).
+static bool sizes_ok(int B, int Hq, int Hkv, int Nq, int Nk, int d)
+{
+    const bool ok = check_shape(B, Hq, Hkv, Nq, Nk, d, 1.f, 0) == FA_OK;
+    t_error.clear();
+    return ok;
+}
+
 fa_status_t fa_fwd_window(fa_dtype_t dtype, const void* q, const void* k, const void* v, void* o, float* lse, int B,
                           int Hq, int Hkv, int Nq, int Nk, int d, float scale, int window, int sinks, void* stream)
 {
     const int w[2] = {window, sinks};
-    return fwd_entry((int)dtype, q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, 1, stream, w);
+    return guarded([&] { return fwd_entry((int)dtype, q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, 1, stream, w); });
 }
 
 size_t fa_bwd_window_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int d, int window, int sinks)
 {
-    if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Nk < 1 || Hq % Hkv != 0 || d < 1 || d > 256 || window < 1 || sinks < 0)
+    if (!sizes_ok(B, Hq, Hkv, Nq, Nk, d) || window < 1 || sinks < 0)
         return 0;
     const Window w{std::min(window, Nk), std::min(sinks, Nk)};
     return bwd_win_plan(bwd_plan(B, Hq, Hkv, Nq, Nk, d), B, Hq, Hkv, Nq, Nk, d, w, sm_count()).total_split;
@@ -2247,7 +2272,7 @@ size_t fa_bwd_window_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int 
 
 int fa_bwd_window_query_split(int B, int Hq, int Hkv, int Nq, int Nk, int d, int window, int sinks, int* sink_split)
 {
-    if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Nk < 1 || Hq % Hkv != 0 || d < 1 || d > 256 || window < 1 || sinks < 0)
+    if (!sizes_ok(B, Hq, Hkv, Nq, Nk, d) || window < 1 || sinks < 0)
         return 0;
     const Window w{std::min(window, Nk), std::min(sinks, Nk)};
     const BwdWinPlan pl = bwd_win_plan(bwd_plan(B, Hq, Hkv, Nq, Nk, d), B, Hq, Hkv, Nq, Nk, d, w, sm_count());
@@ -2262,15 +2287,17 @@ fa_status_t fa_bwd_window(fa_dtype_t dtype, const void* q, const void* k, const 
                           size_t workspace_bytes, void* stream)
 {
     const int w[2] = {window, sinks};
-    return bwd_entry((int)dtype, q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, Nq, Nk, d, scale, 1, workspace,
-                     workspace_bytes, stream, w);
+    return guarded([&] {
+        return bwd_entry((int)dtype, q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, Nq, Nk, d, scale, 1, workspace,
+                         workspace_bytes, stream, w);
+    });
 }
 
 size_t fa_fwd_paged_window_workspace_size(int B, int Hq, int Hkv, int Nq, int page_size, int max_pages_per_seq, int d,
                                           int window, int sinks)
 {
-    if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Hq % Hkv != 0 || d < 1 || page_size < 1 || max_pages_per_seq < 1 ||
-        (long long)page_size * max_pages_per_seq > (1ll << 30) || window < 1 || sinks < 0)
+    if (page_size < 1 || max_pages_per_seq < 1 || (long long)page_size * max_pages_per_seq > (1ll << 30) ||
+        !sizes_ok(B, Hq, Hkv, Nq, page_size * max_pages_per_seq, d) || !decode_shape(Hq, Hkv, Nq, d) || window < 1 || sinks < 0)
         return 0;
     const int max_len = page_size * max_pages_per_seq;
     static const int some = 0;
@@ -2287,41 +2314,43 @@ fa_status_t fa_fwd_paged_window(fa_dtype_t dtype, const void* q, const void* k_c
                                 float scale, int window, int sinks, void* workspace, size_t workspace_bytes,
                                 void* stream)
 {
-    t_error.clear();
-    fa_status_t st;
-    if ((st = check_dtype((int)dtype)) || (st = check_ptr(q, "q")) || (st = check_ptr(k_cache, "k_cache")) ||
-        (st = check_ptr(v_cache, "v_cache")) || (st = check_ptr(o, "o")) || (st = check_float(lse, "lse", true)) ||
-        (st = check_float(block_table, "block_table", false)) || (st = check_float(seq_lens, "seq_lens", false)))
-        return st;
-    if (page_size < 64 || page_size % 64 != 0 || num_pages < 1 || max_pages_per_seq < 1 ||
-        (long long)page_size * max_pages_per_seq > (1ll << 30) || (long long)num_pages * page_size > (1ll << 31)) {
-        set_error("page_size must be a positive multiple of 64; num_pages, max_pages_per_seq >= 1");
-        return FA_ERR_INVALID_ARGUMENT;
-    }
-    const int max_len = page_size * max_pages_per_seq;
-    if ((st = check_shape(B, Hq, Hkv, Nq, max_len, d, scale, 1)) != FA_OK)
-        return st;
-    PagedDesc pg{block_table, seq_lens, page_size, num_pages, max_pages_per_seq};
-    StreamArgs a = stream_args((int)dtype, q, k_cache, v_cache, o, lse, B, Hq, Hkv, Nq, max_len, d, scale, 1);
-    if ((st = check_window(window, sinks, max_len, &a.win)) != FA_OK)
-        return st;
-    if (!decode_shape(Hq, Hkv, Nq, d)) {
-        set_error("paged decode needs d <= 128 and Nq * Hq / Hkv <= %d", kDecodeMaxRows);
-        return FA_ERR_UNSUPPORTED;
-    }
-    if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)) {
-        set_error("workspace is not 256-byte aligned");
-        return FA_ERR_INVALID_ARGUMENT;
-    }
-    a.list = fa::kListPaged;
-    a.lens = seq_lens;
-    a.pg = &pg;
-    return run_stream(a, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+    return guarded([&]() -> fa_status_t {
+        t_error.clear();
+        fa_status_t st;
+        if ((st = check_dtype((int)dtype)) || (st = check_ptr(q, "q")) || (st = check_ptr(k_cache, "k_cache")) ||
+            (st = check_ptr(v_cache, "v_cache")) || (st = check_ptr(o, "o")) || (st = check_float(lse, "lse", true)) ||
+            (st = check_float(block_table, "block_table", false)) || (st = check_float(seq_lens, "seq_lens", false)))
+            return st;
+        if (page_size < 64 || page_size % 64 != 0 || num_pages < 1 || max_pages_per_seq < 1 ||
+            (long long)page_size * max_pages_per_seq > (1ll << 30) || (long long)num_pages * page_size > (1ll << 31)) {
+            set_error("page_size must be a positive multiple of 64; num_pages, max_pages_per_seq >= 1");
+            return FA_ERR_INVALID_ARGUMENT;
+        }
+        const int max_len = page_size * max_pages_per_seq;
+        if ((st = check_shape(B, Hq, Hkv, Nq, max_len, d, scale, 1)) != FA_OK)
+            return st;
+        PagedDesc pg{block_table, seq_lens, page_size, num_pages, max_pages_per_seq};
+        StreamArgs a = stream_args((int)dtype, q, k_cache, v_cache, o, lse, B, Hq, Hkv, Nq, max_len, d, scale, 1);
+        if ((st = check_window(window, sinks, max_len, &a.win)) != FA_OK)
+            return st;
+        if (!decode_shape(Hq, Hkv, Nq, d)) {
+            set_error("paged decode needs d <= 128 and Nq * Hq / Hkv <= %d", kDecodeMaxRows);
+            return FA_ERR_UNSUPPORTED;
+        }
+        if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)) {
+            set_error("workspace is not 256-byte aligned");
+            return FA_ERR_INVALID_ARGUMENT;
+        }
+        a.list = fa::kListPaged;
+        a.lens = seq_lens;
+        a.pg = &pg;
+        return run_stream(a, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+    });
 }
 
 static bool prefix_sizes_ok(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d)
 {
-    return B >= 1 && Hq >= 1 && Hkv >= 1 && Nq >= 1 && Np >= 1 && Ns >= 1 && Hq % Hkv == 0 && d >= 1 && d <= 256;
+    return sizes_ok(B, Hq, Hkv, Nq, Ns, d) && sizes_ok(1, Hq, Hkv, Nq, Np, d) && (long long)Np + Ns <= (1ll << 30);
 }
 
 size_t fa_fwd_prefix_workspace_size(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d)
@@ -2340,194 +2369,202 @@ fa_status_t fa_fwd_prefix(fa_dtype_t dtype, const void* q, const void* k_prefix,
                           int Np, int Ns, int d, float scale, int causal, void* workspace, size_t workspace_bytes,
                           void* stream)
 {
-    t_error.clear();
-    fa_status_t st;
-    if ((st = check_dtype((int)dtype)) || (st = check_ptr(q, "q")) || (st = check_ptr(k_prefix, "k_prefix")) ||
-        (st = check_ptr(v_prefix, "v_prefix")) || (st = check_ptr(k, "k")) || (st = check_ptr(v, "v")) ||
-        (st = check_ptr(o, "o")) || (st = check_float(lse, "lse", true)) || (st = check_float(seq_lens, "seq_lens", true)) ||
-        (st = check_shape(B, Hq, Hkv, Nq, Ns, d, scale, causal)) || (st = check_shape(1, Hq, Hkv, Nq, Np, d, scale, causal)))
+    return guarded([&]() -> fa_status_t {
+        t_error.clear();
+        fa_status_t st;
+        if ((st = check_dtype((int)dtype)) || (st = check_ptr(q, "q")) || (st = check_ptr(k_prefix, "k_prefix")) ||
+            (st = check_ptr(v_prefix, "v_prefix")) || (st = check_ptr(k, "k")) || (st = check_ptr(v, "v")) ||
+            (st = check_ptr(o, "o")) || (st = check_float(lse, "lse", true)) || (st = check_float(seq_lens, "seq_lens", true)) ||
+            (st = check_shape(B, Hq, Hkv, Nq, Ns, d, scale, causal)) || (st = check_shape(1, Hq, Hkv, Nq, Np, d, scale, causal)))
+            return st;
+        if ((long long)Np + Ns > (1ll << 30) || (long long)(Hq / Hkv) * Nq > (1ll << 30)) {
+            set_error("problem too large for 32-bit positions");
+            return FA_ERR_UNSUPPORTED;
+        }
+        if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)) {
+            set_error("workspace is not 256-byte aligned");
+            return FA_ERR_INVALID_ARGUMENT;
+        }
+        const PrefixArgs a{q, k_prefix, v_prefix, k, v, seq_lens, o, lse, B, Hq, Hkv, Nq, Np, Ns, d, scale, causal};
+        const PrefixPlan pl = prefix_plan(a, (int)dtype);
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        void* ws = workspace;
+        if (workspace && workspace_bytes < pl.total) {
+            set_error("workspace has %zu bytes, %zu needed", workspace_bytes, pl.total);
+            return FA_ERR_WORKSPACE;
+        }
+        if (!ws && pl.total > 0) {
+            cudaError_t e = scratch_alloc(&ws, pl.total, s);
+            if (e != cudaSuccess)
+                return cuda_fail(e, "scratch allocation (prefix partials)");
+        }
+        st = dtype == FA_DTYPE_FP16 ? prefix_t<__half>(a, pl, ws, s) : prefix_t<__nv_bfloat16>(a, pl, ws, s);
+        if (ws && !workspace) {
+            cudaError_t e = cudaFreeAsync(ws, s);
+            if (e != cudaSuccess && st == FA_OK)
+                st = cuda_fail(e, "cudaFreeAsync");
+        }
         return st;
-    if ((long long)Np + Ns > (1ll << 30) || (long long)(Hq / Hkv) * Nq > (1ll << 30)) {
-        set_error("problem too large for 32-bit positions");
-        return FA_ERR_UNSUPPORTED;
-    }
-    if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)) {
-        set_error("workspace is not 256-byte aligned");
-        return FA_ERR_INVALID_ARGUMENT;
-    }
-    const PrefixArgs a{q, k_prefix, v_prefix, k, v, seq_lens, o, lse, B, Hq, Hkv, Nq, Np, Ns, d, scale, causal};
-    const PrefixPlan pl = prefix_plan(a, (int)dtype);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    void* ws = workspace;
-    if (workspace && workspace_bytes < pl.total) {
-        set_error("workspace has %zu bytes, %zu needed", workspace_bytes, pl.total);
-        return FA_ERR_WORKSPACE;
-    }
-    if (!ws && pl.total > 0) {
-        cudaError_t e = scratch_alloc(&ws, pl.total, s);
-        if (e != cudaSuccess)
-            return cuda_fail(e, "scratch allocation (prefix partials)");
-    }
-    st = dtype == FA_DTYPE_FP16 ? prefix_t<__half>(a, pl, ws, s) : prefix_t<__nv_bfloat16>(a, pl, ws, s);
-    if (ws && !workspace) {
-        cudaError_t e = cudaFreeAsync(ws, s);
-        if (e != cudaSuccess && st == FA_OK)
-            st = cuda_fail(e, "cudaFreeAsync");
-    }
-    return st;
+    });
 }
 
 fa_status_t fa_key_weights(fa_dtype_t dtype, const void* q, const void* k, const float* lse, const float* weights_in,
                            float* weights_out, int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, int causal,
                            void* stream)
 {
-    t_error.clear();
-    fa_status_t st;
-    if ((st = check_dtype((int)dtype)) || (st = check_ptr(q, "q")) || (st = check_ptr(k, "k")) ||
-        (st = check_float(lse, "lse", false)) || (st = check_shape(B, Hq, Hkv, Nq, Nk, d, scale, causal)) ||
-        (st = check_weights(weights_in, weights_out, (size_t)B * Hkv * Nk)))
-        return st;
-    return key_weights((int)dtype, q, k, lse, weights_in, weights_out, B, Hq, Hkv, Nq, Nk, d, scale, causal,
-                       static_cast<cudaStream_t>(stream));
+    return guarded([&]() -> fa_status_t {
+        t_error.clear();
+        fa_status_t st;
+        if ((st = check_dtype((int)dtype)) || (st = check_ptr(q, "q")) || (st = check_ptr(k, "k")) ||
+            (st = check_float(lse, "lse", false)) || (st = check_shape(B, Hq, Hkv, Nq, Nk, d, scale, causal)) ||
+            (st = check_weights(weights_in, weights_out, (size_t)B * Hkv * Nk)))
+            return st;
+        return key_weights((int)dtype, q, k, lse, weights_in, weights_out, B, Hq, Hkv, Nq, Nk, d, scale, causal,
+                           static_cast<cudaStream_t>(stream));
+    });
 }
 
 fa_status_t fa_fwd_weights(fa_dtype_t dtype, const void* q, const void* k, const void* v, void* o, float* lse,
                            const float* weights_in, float* weights_out, int B, int Hq, int Hkv, int Nq, int Nk, int d,
                            float scale, int causal, void* stream)
 {
-    t_error.clear();
-    fa_status_t st;
-    if ((st = check_dtype((int)dtype)) || (st = check_ptr(q, "q")) || (st = check_ptr(k, "k")) ||
-        (st = check_ptr(v, "v")) || (st = check_ptr(o, "o")) || (st = check_float(lse, "lse", true)) ||
-        (st = check_shape(B, Hq, Hkv, Nq, Nk, d, scale, causal)) ||
-        (st = check_weights(weights_in, weights_out, (size_t)B * Hkv * Nk)))
-        return st;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    void* ws = nullptr;
-    if (decode_shape(Hq, Hkv, Nq, d)) {
-        StreamArgs a = stream_args((int)dtype, q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal);
-        const StreamPlan pl = stream_plan(a);
-        const size_t rows = (size_t)B * Hq * Nq, stride = ((size_t)Nk + 63) / 64 * 64;
-        const size_t lse_off = pl.total + align256(rows * stride * 4);
-        cudaError_t e = scratch_alloc(&ws, lse_off + (lse ? 0 : rows * 4), s);
-        if (e != cudaSuccess)
-            return cuda_fail(e, "scratch allocation (decode partials and scores)");
-        char* w = static_cast<char*>(ws);
-        a.scores = reinterpret_cast<float*>(w + pl.total);
-        a.score_stride = (int)stride;
-        if (!lse)
-            a.lse = reinterpret_cast<float*>(w + lse_off);
-        st = launch_stream_any(a, pl, ws, s);
-        if (st == FA_OK) {
-            fa::DecodeWeightParams p;
-            p.scores = a.scores;
-            p.lse = a.lse;
-            p.w_in = weights_in;
-            p.w_out = weights_out;
-            p.BH = B * Hkv;
-            p.R = Hq / Hkv * Nq;
-            p.Nk = Nk;
-            p.stride = a.score_stride;
-            const long long blocks = (long long)p.BH * ((Nk + 511) / 512);
-            st = launch_dependent("decode_weights_kernel launch", fa::decode_weights_kernel, dim3((unsigned)blocks),
-                                  dim3(128), 0, s, p);
-        }
-    } else {
-        float* l = lse;
-        if (!l) {
-            cudaError_t e = scratch_alloc(&ws, (size_t)B * Hq * Nq * 4, s);
+    return guarded([&]() -> fa_status_t {
+        t_error.clear();
+        fa_status_t st;
+        if ((st = check_dtype((int)dtype)) || (st = check_ptr(q, "q")) || (st = check_ptr(k, "k")) ||
+            (st = check_ptr(v, "v")) || (st = check_ptr(o, "o")) || (st = check_float(lse, "lse", true)) ||
+            (st = check_shape(B, Hq, Hkv, Nq, Nk, d, scale, causal)) ||
+            (st = check_weights(weights_in, weights_out, (size_t)B * Hkv * Nk)))
+            return st;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        void* ws = nullptr;
+        if (decode_shape(Hq, Hkv, Nq, d)) {
+            StreamArgs a = stream_args((int)dtype, q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, causal);
+            const StreamPlan pl = stream_plan(a);
+            const size_t rows = (size_t)B * Hq * Nq, stride = ((size_t)Nk + 63) / 64 * 64;
+            const size_t lse_off = pl.total + align256(rows * stride * 4);
+            cudaError_t e = scratch_alloc(&ws, lse_off + (lse ? 0 : rows * 4), s);
             if (e != cudaSuccess)
-                return cuda_fail(e, "scratch allocation (log-sum-exp)");
-            l = static_cast<float*>(ws);
+                return cuda_fail(e, "scratch allocation (decode partials and scores)");
+            char* w = static_cast<char*>(ws);
+            a.scores = reinterpret_cast<float*>(w + pl.total);
+            a.score_stride = (int)stride;
+            if (!lse)
+                a.lse = reinterpret_cast<float*>(w + lse_off);
+            st = launch_stream_any(a, pl, ws, s);
+            if (st == FA_OK) {
+                fa::DecodeWeightParams p;
+                p.scores = a.scores;
+                p.lse = a.lse;
+                p.w_in = weights_in;
+                p.w_out = weights_out;
+                p.BH = B * Hkv;
+                p.R = Hq / Hkv * Nq;
+                p.Nk = Nk;
+                p.stride = a.score_stride;
+                const long long blocks = (long long)p.BH * ((Nk + 511) / 512);
+                st = launch_dependent("decode_weights_kernel launch", fa::decode_weights_kernel, dim3((unsigned)blocks),
+                                      dim3(128), 0, s, p);
+            }
+        } else {
+            float* l = lse;
+            if (!l) {
+                cudaError_t e = scratch_alloc(&ws, (size_t)B * Hq * Nq * 4, s);
+                if (e != cudaSuccess)
+                    return cuda_fail(e, "scratch allocation (log-sum-exp)");
+                l = static_cast<float*>(ws);
+            }
+            st = fwd_tiled((int)dtype, q, k, v, o, l, B, Hq, Hkv, Nq, Nk, d, scale, causal, s);
+            if (st == FA_OK)
+                st = key_weights((int)dtype, q, k, l, weights_in, weights_out, B, Hq, Hkv, Nq, Nk, d, scale, causal, s);
         }
-        st = fwd_tiled((int)dtype, q, k, v, o, l, B, Hq, Hkv, Nq, Nk, d, scale, causal, s);
-        if (st == FA_OK)
-            st = key_weights((int)dtype, q, k, l, weights_in, weights_out, B, Hq, Hkv, Nq, Nk, d, scale, causal, s);
-    }
-    if (ws) {
-        cudaError_t e = cudaFreeAsync(ws, s);
-        if (e != cudaSuccess && st == FA_OK)
-            st = cuda_fail(e, "cudaFreeAsync");
-    }
-    return st;
+        if (ws) {
+            cudaError_t e = cudaFreeAsync(ws, s);
+            if (e != cudaSuccess && st == FA_OK)
+                st = cuda_fail(e, "cudaFreeAsync");
+        }
+        return st;
+    });
 }
 
 fa_status_t fa_kv_evict(fa_dtype_t dtype, const void* k, const void* v, const float* weights, const int* seq_lens,
                         void* k_out, void* v_out, float* weights_out, int* index_out, int B, int Hkv, int Nk, int d,
                         int keep, int recent, void* stream)
 {
-    t_error.clear();
-    fa_status_t st;
-    if ((st = check_dtype((int)dtype)) || (st = check_ptr(k, "k")) || (st = check_ptr(v, "v")) ||
-        (st = check_float(weights, "weights", false)) || (st = check_float(seq_lens, "seq_lens", true)) ||
-        (st = check_ptr(k_out, "k_out")) || (st = check_ptr(v_out, "v_out")) ||
-        (st = check_float(weights_out, "weights_out", true)) || (st = check_float(index_out, "index_out", true)) ||
-        (st = check_shape(B, Hkv, Hkv, 1, Nk, d, 1.f, 0)))
+    return guarded([&]() -> fa_status_t {
+        t_error.clear();
+        fa_status_t st;
+        if ((st = check_dtype((int)dtype)) || (st = check_ptr(k, "k")) || (st = check_ptr(v, "v")) ||
+            (st = check_float(weights, "weights", false)) || (st = check_float(seq_lens, "seq_lens", true)) ||
+            (st = check_ptr(k_out, "k_out")) || (st = check_ptr(v_out, "v_out")) ||
+            (st = check_float(weights_out, "weights_out", true)) || (st = check_float(index_out, "index_out", true)) ||
+            (st = check_shape(B, Hkv, Hkv, 1, Nk, d, 1.f, 0)))
+            return st;
+        if (keep < 1 || recent < 0 || recent > keep) {
+            set_error("keep=%d must be >= 1 and recent=%d in [0, keep]", keep, recent);
+            return FA_ERR_INVALID_ARGUMENT;
+        }
+        const size_t BH = (size_t)B * Hkv, in_bytes = BH * Nk * d * 2, out_bytes = BH * keep * d * 2;
+        if ((long long)keep * (d / 8) > (1ll << 31) - 4096 ||
+            BH * (((size_t)keep * (d / 8) + 1023) / 1024) > (size_t)(1u << 31) - 1) {
+            set_error("keep=%d is too large for 32-bit indices", keep);
+            return FA_ERR_UNSUPPORTED;
+        }
+        const struct {
+            const void* p;
+            size_t n;
+            bool out;
+        } bufs[] = {{k, in_bytes, false},      {v, in_bytes, false},       {weights, BH * Nk * 4, false}, {seq_lens, (size_t)B * 4, false},
+                    {k_out, out_bytes, true},  {v_out, out_bytes, true},   {weights_out, BH * keep * 4, true},
+                    {index_out, BH * keep * 4, true}};
+        for (int i = 0; i < 8; ++i)
+            for (int j = i + 1; j < 8; ++j)
+                if ((bufs[i].out || bufs[j].out) && overlap(bufs[i].p, bufs[i].n, bufs[j].p, bufs[j].n)) {
+                    set_error("an output overlaps an input or another output");
+                    return FA_ERR_INVALID_ARGUMENT;
+                }
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        void* ws = nullptr;
+        if (!index_out) {
+            cudaError_t e = scratch_alloc(&ws, BH * keep * 4, s);
+            if (e != cudaSuccess)
+                return cuda_fail(e, "scratch allocation (kept indices)");
+        }
+        fa::EvictParams p = {};
+        p.w = weights;
+        p.seq_lens = seq_lens;
+        p.k = static_cast<const uint4*>(k);
+        p.v = static_cast<const uint4*>(v);
+        p.k_out = static_cast<uint4*>(k_out);
+        p.v_out = static_cast<uint4*>(v_out);
+        p.w_out = weights_out;
+        p.index = index_out ? index_out : static_cast<int*>(ws);
+        p.BH = (int)BH;
+        p.Hkv = Hkv;
+        p.Nk = Nk;
+        p.chunks = d / 8;
+        p.keep = keep;
+        p.recent = recent;
+        const int cache = (std::min(Nk, fa::kEvictCache) + fa::kEvictList) * 4;
+        const bool fused = (size_t)keep * d * 4 <= kEvictFusedBytes;
+        auto select = fused ? fa::evict_select_kernel<true> : fa::evict_select_kernel<false>;
+        st = ensure_smem(reinterpret_cast<const void*>(select), (fa::kEvictCache + fa::kEvictList) * 4);
+        if (st == FA_OK) {
+            select<<<(unsigned)BH, fa::kEvictThreads, cache, s>>>(p);
+            st = check_launch("evict_select_kernel launch");
+        }
+        if (st == FA_OK && !fused) {
+            const size_t per = ((size_t)keep * p.chunks + 256 * fa::kGatherItems - 1) / (256 * fa::kGatherItems);
+            st = launch_dependent("evict_gather_kernel launch", fa::evict_gather_kernel, dim3((unsigned)(BH * per)), dim3(256),
+                                  0, s, p);
+        }
+        if (ws) {
+            cudaError_t e = cudaFreeAsync(ws, s);
+            if (e != cudaSuccess && st == FA_OK)
+                st = cuda_fail(e, "cudaFreeAsync");
+        }
         return st;
-    if (keep < 1 || recent < 0 || recent > keep) {
-        set_error("keep=%d must be >= 1 and recent=%d in [0, keep]", keep, recent);
-        return FA_ERR_INVALID_ARGUMENT;
-    }
-    const size_t BH = (size_t)B * Hkv, in_bytes = BH * Nk * d * 2, out_bytes = BH * keep * d * 2;
-    if ((long long)keep * (d / 8) > (1ll << 31) - 4096 ||
-        BH * (((size_t)keep * (d / 8) + 1023) / 1024) > (size_t)(1u << 31) - 1) {
-        set_error("keep=%d is too large for 32-bit indices", keep);
-        return FA_ERR_UNSUPPORTED;
-    }
-    const struct {
-        const void* p;
-        size_t n;
-        bool out;
-    } bufs[] = {{k, in_bytes, false},      {v, in_bytes, false},       {weights, BH * Nk * 4, false}, {seq_lens, (size_t)B * 4, false},
-                {k_out, out_bytes, true},  {v_out, out_bytes, true},   {weights_out, BH * keep * 4, true},
-                {index_out, BH * keep * 4, true}};
-    for (int i = 0; i < 8; ++i)
-        for (int j = i + 1; j < 8; ++j)
-            if ((bufs[i].out || bufs[j].out) && overlap(bufs[i].p, bufs[i].n, bufs[j].p, bufs[j].n)) {
-                set_error("an output overlaps an input or another output");
-                return FA_ERR_INVALID_ARGUMENT;
-            }
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    void* ws = nullptr;
-    if (!index_out) {
-        cudaError_t e = scratch_alloc(&ws, BH * keep * 4, s);
-        if (e != cudaSuccess)
-            return cuda_fail(e, "scratch allocation (kept indices)");
-    }
-    fa::EvictParams p = {};
-    p.w = weights;
-    p.seq_lens = seq_lens;
-    p.k = static_cast<const uint4*>(k);
-    p.v = static_cast<const uint4*>(v);
-    p.k_out = static_cast<uint4*>(k_out);
-    p.v_out = static_cast<uint4*>(v_out);
-    p.w_out = weights_out;
-    p.index = index_out ? index_out : static_cast<int*>(ws);
-    p.BH = (int)BH;
-    p.Hkv = Hkv;
-    p.Nk = Nk;
-    p.chunks = d / 8;
-    p.keep = keep;
-    p.recent = recent;
-    const int cache = (std::min(Nk, fa::kEvictCache) + fa::kEvictList) * 4;
-    const bool fused = (size_t)keep * d * 4 <= kEvictFusedBytes;
-    auto select = fused ? fa::evict_select_kernel<true> : fa::evict_select_kernel<false>;
-    st = ensure_smem(reinterpret_cast<const void*>(select), (fa::kEvictCache + fa::kEvictList) * 4);
-    if (st == FA_OK) {
-        select<<<(unsigned)BH, fa::kEvictThreads, cache, s>>>(p);
-        st = check_launch("evict_select_kernel launch");
-    }
-    if (st == FA_OK && !fused) {
-        const size_t per = ((size_t)keep * p.chunks + 256 * fa::kGatherItems - 1) / (256 * fa::kGatherItems);
-        st = launch_dependent("evict_gather_kernel launch", fa::evict_gather_kernel, dim3((unsigned)(BH * per)), dim3(256),
-                              0, s, p);
-    }
-    if (ws) {
-        cudaError_t e = cudaFreeAsync(ws, s);
-        if (e != cudaSuccess && st == FA_OK)
-            st = cuda_fail(e, "cudaFreeAsync");
-    }
-    return st;
+    });
 }
 
 fa_status_t fa_check_device_status(void* stream)

@@ -51,6 +51,12 @@ CASES = [
     (2, 4, 1, 100, 3, 7, 64, [7, 0]),                    # rows far longer than all keys: some see nothing
     (2, 4, 1, 3, 1, 2, 128, [2, 0]),
     (64, 4, 2, 1, 5000, 40, 128, None),                  # key shares of the prefix
+    # packed tiles with the split-KV pass for the own keys (prefixes too long to be read per sequence)
+    (70, 16, 8, 1, 520, 140, 64, [(31 * i) % 141 for i in range(70)]),
+    (67, 8, 8, 2, 513, 300, 128, [300] * 3 + [1, 0, 2] * 20 + [299] * 4),
+    (33, 32, 2, 1, 4100, 5, 96, [i % 6 for i in range(33)]),
+    (130, 4, 4, 1, 520, 64, 32, [0] * 129 + [64]),
+    (130, 4, 4, 1, 520, 64, 32, [0] * 130),
 ]
 
 
@@ -108,9 +114,9 @@ def test_matches_the_concatenated_cache():
     assert (lse - l1).abs().max() <= 1e-5
 
 
-@pytest.mark.parametrize("Nq", [1, 9, 64])
-def test_graph_streams_and_repeats(Nq):
-    shape = (6, 8, 2, Nq, 900, 100, 128)
+@pytest.mark.parametrize("Nq,Np", [(1, 900), (1, 33000), (9, 900), (64, 900)])
+def test_graph_streams_and_repeats(Nq, Np):
+    shape = (6, 8, 2, Nq, Np, 100, 128)
     q, kp, vp, k, v = make_prefix(*shape, BF16, 3300)
     q2, kp2, vp2, k2, v2 = make_prefix(*shape, BF16, 3400)
     ln = torch.tensor([100, 64, 70, 80, 90, 99], dtype=torch.int32, device="cuda")
