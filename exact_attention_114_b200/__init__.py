@@ -401,54 +401,37 @@ def fa_bwd(q, k, v, o, dout, lse, dq=None, dk=None, dv=None, *, causal=False, sc
 
 
 _NO_CONTEXT = contextlib.nullcontext()
-_CODES = {}   # 16-bit torch dtype -> FA_DTYPE_*; filled with the first call, which imports torch
+# What the calls below need of torch, bound once (a call's host time is a few microseconds, of which
+# looking these up again would be a part): filled by _bind().
+_codes = _f32 = _i32 = _empty_like = _current_device = _current_stream = None
 
 
-def _code_of(dtype):
-    code = _CODES.get(dtype)
+def _bind():
+    global _codes, _f32, _i32, _empty_like, _current_device, _current_stream
+    import torch
+    _f32, _i32, _empty_like = torch.float32, torch.int32, torch.empty_like
+    _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _codes = {torch.bfloat16: FA_DTYPE_BF16, torch.float16: FA_DTYPE_FP16}
+
+
+def _start(t, name):
+    """(FA_DTYPE_* code, element type, device index) of a call's first tensor."""
+    if _codes is None:
+        _bind()
+    dtype, dev = t.dtype, t.get_device()
+    code = _codes.get(dtype)
     if code is None:
-        import torch
-        _CODES.update({torch.bfloat16: FA_DTYPE_BF16, torch.float16: FA_DTYPE_FP16})
-        code = _CODES.get(dtype)
-        if code is None:
-            raise ValueError(f"unsupported dtype {dtype} (bf16 or fp16)")
-    return code
-
-
-def _on_device(stream, dev):
-    """A context in which `dev` (and `stream`, if given) is current, so that outputs are allocated and
-    kernels launched there."""
-    import torch
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream is of {stream.device}, the tensors on {dev}")
-        return torch.cuda.stream(stream)
-    if dev.index != torch._C._cuda_getDevice():
-        return torch.cuda.device(dev)
-    return _NO_CONTEXT
-
-
-def _raw_stream(dev):
-    """Handle of `dev`'s current stream (without the object that torch.cuda.current_stream() makes)."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev.index)
-
-
-def _leader(t, name):
-    """The device of a call's first tensor."""
-    if not t.is_cuda:
+        raise ValueError(f"unsupported dtype {dtype} (bf16 or fp16)")
+    if dev < 0:
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    return t.device
+    return code, dtype, dev
 
 
 def _expect(t, name, dev, dtype, shape=None):
-    """Pointer of a contiguous tensor of `dtype` (and `shape`) on `dev`; None stays None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
+    """Pointer of a contiguous tensor of `dtype` (and `shape`) on device `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or (shape is not None and t.shape != shape):
         _require(t, name, dtype, shape)
-    if t.device != dev:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}, it is on {t.device}")
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on cuda:{dev}, it is on {t.device}")
     return t.data_ptr()
 
 
@@ -457,9 +440,23 @@ def _workspace(t, dev):
     if t is None:
         return None, 0
     n = _ws_bytes(t)
-    if t.device != dev:
-        raise ValueError(f"workspace is on {t.device}, the tensors on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"workspace is on {t.device}, the tensors on cuda:{dev}")
     return t.data_ptr(), n
+
+
+def _on_device(stream, dev):
+    """A context in which device `dev` (and `stream`, if given) is current, so that outputs are allocated
+    and kernels launched there."""
+    if stream is None:
+        if dev == _current_device():
+            return _NO_CONTEXT
+        import torch
+        return torch.cuda.device(dev)
+    import torch
+    if stream.device.index != dev:
+        raise ValueError(f"stream is of {stream.device}, the tensors on cuda:{dev}")
+    return torch.cuda.stream(stream)
 
 
 def _scale(scale, d):
@@ -467,34 +464,45 @@ def _scale(scale, d):
 
 
 def _qkv(q, k, v):
-    """Device, dtype code, sizes and pointers of q, k and v."""
-    sq, sk, dt = q.shape, k.shape, q.dtype
-    if len(sq) != 4 or len(sk) != 4 or sq[0] != sk[0] or sq[3] != sk[3]:
-        raise ValueError(f"q {tuple(sq)} and k {tuple(sk)} disagree")
-    code, dev = _code_of(dt), _leader(q, "q")
+    """Device, dtype code, element type, sizes and pointers of q, k and v."""
+    code, dt, dev = _start(q, "q")
+    sk = k.shape
+    if q.dim() != 4 or len(sk) != 4:
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(sk)} must have four dimensions")
+    B, Hq, Nq, d = q.shape
+    if sk[0] != B or sk[3] != d:
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(sk)} disagree")
     ptrs = (_expect(q, "q", dev, dt), _expect(k, "k", dev, dt), _expect(v, "v", dev, dt, sk))
-    return dev, code, (sq[0], sq[1], sk[1], sq[2], sk[2], sq[3]), ptrs
+    return dev, code, dt, (B, Hq, sk[1], Nq, sk[2], d), ptrs
 
 
-def _new_lse(q):
-    import torch
-    return q.new_empty(q.shape[:3], dtype=torch.float32)
+def _out(t, name, q, dev, dt):
+    """(tensor, pointer) of an output like q: the one given, or a new one."""
+    if t is None:
+        t = _empty_like(q)
+        return t, t.data_ptr()
+    return t, _expect(t, name, dev, dt, q.shape)
+
+
+def _out_lse(t, q, sizes, dev):
+    shape = (sizes[0], sizes[1], sizes[3])
+    if t is None:
+        t = q.new_empty(shape, dtype=_f32)
+        return t, t.data_ptr()
+    return t, _expect(t, "lse", dev, _f32, shape)
 
 
 def fa_fwd_window(q, k, v, window, sinks=0, o=None, lse=None, *, scale=None, stream=None, want_lse=True):
     """Forward with a sliding window and sinks (causal): each query sees the ``window`` newest keys
     up to its own and the first ``sinks`` keys.  bf16 or fp16; returns (o, lse)."""
-    import torch
-    dev, code, sizes, ptrs = _qkv(q, k, v)
-    _expect(o, "o", dev, q.dtype, q.shape)
-    _expect(lse, "lse", dev, torch.float32, q.shape[:3])
+    dev, code, dt, sizes, ptrs = _qkv(q, k, v)
     with _on_device(stream, dev):
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = _new_lse(q)
-        _check(lib().fa_fwd_window(code, *ptrs, o.data_ptr(), None if lse is None else lse.data_ptr(), *sizes,
-                                   _scale(scale, sizes[5]), int(window), int(sinks), _raw_stream(dev)))
+        o, po = _out(o, "o", q, dev, dt)
+        pl = None
+        if lse is not None or want_lse:
+            lse, pl = _out_lse(lse, q, sizes, dev)
+        _check(lib().fa_fwd_window(code, *ptrs, po, pl, *sizes, _scale(scale, sizes[5]), int(window), int(sinks),
+                                   _current_stream(dev)))
     return o, lse
 
 
@@ -513,20 +521,17 @@ def fa_bwd_window_query_split(B, Hq, Hkv, Nq, Nk, d, window, sinks=0):
 def fa_bwd_window(q, k, v, o, dout, lse, window, sinks=0, dq=None, dk=None, dv=None, *, scale=None,
                   workspace=None, stream=None):
     """Backward of ``fa_fwd_window``: returns (dq, dk, dv).  Allocates the gradients when not given."""
-    import torch
-    dev, code, sizes, ptrs = _qkv(q, k, v)
-    dt = q.dtype
-    ptrs += (_expect(o, "o", dev, dt, q.shape), _expect(dout, "dout", dev, dt, q.shape),
-             _expect(lse, "lse", dev, torch.float32, q.shape[:3]))
-    for t, n, ref in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
-        _expect(t, n, dev, dt, ref.shape)
+    dev, code, dt, sizes, ptrs = _qkv(q, k, v)
+    shape = q.shape
+    ptrs += (_expect(o, "o", dev, dt, shape), _expect(dout, "dout", dev, dt, shape),
+             _expect(lse, "lse", dev, _f32, shape[:3]))
     ws = _workspace(workspace, dev)
     with _on_device(stream, dev):
-        dq = torch.empty_like(q) if dq is None else dq
-        dk = torch.empty_like(k) if dk is None else dk
-        dv = torch.empty_like(v) if dv is None else dv
-        _check(lib().fa_bwd_window(code, *ptrs, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *sizes,
-                                   _scale(scale, sizes[5]), int(window), int(sinks), *ws, _raw_stream(dev)))
+        dq, pq = _out(dq, "dq", q, dev, dt)
+        dk, pk = _out(dk, "dk", k, dev, dt)
+        dv, pv = _out(dv, "dv", k, dev, dt)
+        _check(lib().fa_bwd_window(code, *ptrs, pq, pk, pv, *sizes, _scale(scale, sizes[5]), int(window), int(sinks),
+                                   *ws, _current_stream(dev)))
     return dq, dk, dv
 
 
@@ -539,27 +544,22 @@ def fa_fwd_paged_window(q, k_cache, v_cache, block_table, seq_lens, window, sink
                         scale=None, workspace=None, stream=None):
     """``fa_fwd_window`` for single tokens (or the last few) over a paged KV cache: arguments as
     ``fa_fwd_paged``, the window against each sequence's own length."""
-    import torch
+    code, dt, dev = _start(q, "q")
     B, Hq, Nq, d = q.shape
     num_pages, page_size, Hkv, dk = k_cache.shape
-    code, dev, dt = _code_of(q.dtype), _leader(q, "q"), q.dtype
     if dk != d or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache / v_cache shapes disagree with q")
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, max_pages_per_seq]")
     ptrs = (_expect(q, "q", dev, dt), _expect(k_cache, "k_cache", dev, dt), _expect(v_cache, "v_cache", dev, dt),
-            _expect(block_table, "block_table", dev, torch.int32), _expect(seq_lens, "seq_lens", dev, torch.int32, (B,)))
-    _expect(o, "o", dev, dt, q.shape)
-    _expect(lse, "lse", dev, torch.float32, q.shape[:3])
+            _expect(block_table, "block_table", dev, _i32), _expect(seq_lens, "seq_lens", dev, _i32, (B,)))
     ws = _workspace(workspace, dev)
     with _on_device(stream, dev):
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None:
-            lse = _new_lse(q)
-        _check(lib().fa_fwd_paged_window(code, *ptrs, o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, d, page_size,
-                                         num_pages, block_table.shape[1], _scale(scale, d), int(window), int(sinks),
-                                         *ws, _raw_stream(dev)))
+        o, po = _out(o, "o", q, dev, dt)
+        lse, pl = _out_lse(lse, q, (B, Hq, Hkv, Nq), dev)
+        _check(lib().fa_fwd_paged_window(code, *ptrs, po, pl, B, Hq, Hkv, Nq, d, page_size, num_pages,
+                                         block_table.shape[1], _scale(scale, d), int(window), int(sinks), *ws,
+                                         _current_stream(dev)))
     return o, lse
 
 
@@ -573,41 +573,42 @@ def fa_fwd_prefix(q, k_prefix, v_prefix, k, v, seq_lens=None, o=None, lse=None, 
     [Hkv, Np, d], own keys k / v [B, Hkv, Ns, d] of which sequence b holds the first
     ``seq_lens[b]`` (int32 [B]; all without it).  Returns (o, lse), as ``fa_fwd`` on the
     concatenated keys would."""
-    import torch
-    dev, code, (B, Hq, Hkv, Nq, Ns, d), (qp, kp, vp) = _qkv(q, k, v)
-    dt = q.dtype
-    if k_prefix.dim() != 3 or k_prefix.shape[0] != Hkv or k_prefix.shape[2] != d:
-        raise ValueError(f"k_prefix has shape {tuple(k_prefix.shape)}, expected ({Hkv}, Np, {d})")
-    ptrs = (qp, _expect(k_prefix, "k_prefix", dev, dt), _expect(v_prefix, "v_prefix", dev, dt, k_prefix.shape), kp, vp,
-            _expect(seq_lens, "seq_lens", dev, torch.int32, (B,)))
-    _expect(o, "o", dev, dt, q.shape)
-    _expect(lse, "lse", dev, torch.float32, q.shape[:3])
+    dev, code, dt, sizes, (pq, pk, pv) = _qkv(q, k, v)
+    B, Hq, Hkv, Nq, Ns, d = sizes
+    sp = k_prefix.shape
+    if len(sp) != 3 or sp[0] != Hkv or sp[2] != d:
+        raise ValueError(f"k_prefix has shape {tuple(sp)}, expected ({Hkv}, Np, {d})")
+    ptrs = (pq, _expect(k_prefix, "k_prefix", dev, dt), _expect(v_prefix, "v_prefix", dev, dt, sp), pk, pv,
+            None if seq_lens is None else _expect(seq_lens, "seq_lens", dev, _i32, (B,)))
     ws = _workspace(workspace, dev)
     with _on_device(stream, dev):
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None:
-            lse = _new_lse(q)
-        _check(lib().fa_fwd_prefix(code, *ptrs, o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, k_prefix.shape[1], Ns, d,
-                                   _scale(scale, d), int(bool(causal)), *ws, _raw_stream(dev)))
+        o, po = _out(o, "o", q, dev, dt)
+        lse, pl = _out_lse(lse, q, sizes, dev)
+        _check(lib().fa_fwd_prefix(code, *ptrs, po, pl, B, Hq, Hkv, Nq, sp[1], Ns, d, _scale(scale, d),
+                                   1 if causal else 0, *ws, _current_stream(dev)))
     return o, lse
+
+
+def _weights_io(weights, weights_out, k, dev):
+    """Pointer of ``weights`` (or None), and (tensor, pointer) of ``weights_out``, new if None."""
+    shape = k.shape[:3]
+    w = None if weights is None else _expect(weights, "weights", dev, _f32, shape)
+    if weights_out is None:
+        weights_out = k.new_empty(shape, dtype=_f32)
+        return w, weights_out, weights_out.data_ptr()
+    return w, weights_out, _expect(weights_out, "weights_out", dev, _f32, shape)
 
 
 def fa_key_weights(q, k, lse, weights=None, weights_out=None, *, causal=False, scale=None, stream=None):
     """The weight each key receives from the rows of q, added to ``weights`` [B, Hkv, Nk] fp32 (zeros
     if None): returns ``weights_out`` (a new tensor unless given; it may be ``weights`` itself).
     ``lse`` is that of the forward of the same q, k, scale and causal flag."""
-    import torch
-    sizes = B, Hq, Hkv, Nq, Nk, d = _dims(q, k)
-    code, dev, f32 = _code_of(q.dtype), _leader(q, "q"), torch.float32
-    ptrs = (_expect(q, "q", dev, q.dtype), _expect(k, "k", dev, q.dtype), _expect(lse, "lse", dev, f32, (B, Hq, Nq)),
-            _expect(weights, "weights", dev, f32, k.shape[:3]))
-    _expect(weights_out, "weights_out", dev, f32, k.shape[:3])
+    dev, code, dt, sizes, ptrs = _qkv(q, k, k)
+    pl = _expect(lse, "lse", dev, _f32, q.shape[:3])
     with _on_device(stream, dev):
-        if weights_out is None:
-            weights_out = k.new_empty(k.shape[:3], dtype=f32)
-        _check(lib().fa_key_weights(code, *ptrs, weights_out.data_ptr(), *sizes, _scale(scale, d), int(bool(causal)),
-                                    _raw_stream(dev)))
+        w, weights_out, pw = _weights_io(weights, weights_out, k, dev)
+        _check(lib().fa_key_weights(code, ptrs[0], ptrs[1], pl, w, pw, *sizes, _scale(scale, sizes[5]),
+                                    1 if causal else 0, _current_stream(dev)))
     return weights_out
 
 
@@ -616,22 +617,13 @@ def fa_fwd_weights(q, k, v, weights=None, weights_out=None, o=None, lse=None, *,
     """Forward that also adds up the weight each key receives: returns (o, lse, weights_out), the last
     ``weights`` [B, Hkv, Nk] fp32 (zeros if None) plus this call's, in a new tensor unless
     ``weights_out`` is given (it may be ``weights`` itself)."""
-    import torch
-    dev, code, sizes, ptrs = _qkv(q, k, v)
-    f32 = torch.float32
-    _expect(o, "o", dev, q.dtype, q.shape)
-    _expect(lse, "lse", dev, f32, q.shape[:3])
-    w = _expect(weights, "weights", dev, f32, k.shape[:3])
-    _expect(weights_out, "weights_out", dev, f32, k.shape[:3])
+    dev, code, dt, sizes, ptrs = _qkv(q, k, v)
     with _on_device(stream, dev):
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None:
-            lse = _new_lse(q)
-        if weights_out is None:
-            weights_out = k.new_empty(k.shape[:3], dtype=f32)
-        _check(lib().fa_fwd_weights(code, *ptrs, o.data_ptr(), lse.data_ptr(), w, weights_out.data_ptr(), *sizes,
-                                    _scale(scale, sizes[5]), int(bool(causal)), _raw_stream(dev)))
+        o, po = _out(o, "o", q, dev, dt)
+        lse, pl = _out_lse(lse, q, sizes, dev)
+        w, weights_out, pw = _weights_io(weights, weights_out, k, dev)
+        _check(lib().fa_fwd_weights(code, *ptrs, po, pl, w, pw, *sizes, _scale(scale, sizes[5]), 1 if causal else 0,
+                                    _current_stream(dev)))
     return o, lse, weights_out
 
 
@@ -641,34 +633,30 @@ def fa_kv_evict(k, v, weights, keep, recent=0, seq_lens=None, k_out=None, v_out=
     the others, in order.  k, v [B, Hkv, Nk, d], weights [B, Hkv, Nk] fp32, ``seq_lens`` int32 [B] or
     None.  Returns (k_out, v_out, weights_out, index_out).  Of a sequence shorter than ``keep`` the rows
     behind its last key are left as they were; in outputs allocated here they are 0 (index -1)."""
-    import torch
-    if k.dim() != 4:
+    code, dt, dev = _start(k, "k")
+    shape = k.shape
+    if len(shape) != 4:
         raise ValueError("k must be a contiguous CUDA tensor [B, Hkv, Nk, d]")
-    code, dev, dt, f32 = _code_of(k.dtype), _leader(k, "k"), k.dtype, torch.float32
-    B, Hkv, Nk, d = k.shape
+    B, Hkv, Nk, d = shape
     keep, recent = int(keep), int(recent)
     if not 0 <= recent <= keep or keep < 1:
         raise ValueError(f"keep={keep} must be >= 1 and recent={recent} in [0, keep]")
-    ptrs = (_expect(k, "k", dev, dt), _expect(v, "v", dev, dt, k.shape), _expect(weights, "weights", dev, f32, k.shape[:3]),
-            _expect(seq_lens, "seq_lens", dev, torch.int32, (B,)))
-    _expect(k_out, "k_out", dev, dt, (B, Hkv, keep, d))
-    _expect(v_out, "v_out", dev, dt, (B, Hkv, keep, d))
-    _expect(weights_out, "weights_out", dev, f32, (B, Hkv, keep))
-    _expect(index_out, "index_out", dev, torch.int32, (B, Hkv, keep))
-    with _on_device(stream, dev):
-        def new(t, shape, dtype, fill):
-            if t is not None:
-                return t
-            if seq_lens is None and keep <= Nk:   # every row is written
-                return k.new_empty(shape, dtype=dtype)
-            return k.new_full(shape, fill, dtype=dtype)
+    ptrs = (_expect(k, "k", dev, dt), _expect(v, "v", dev, dt, shape), _expect(weights, "weights", dev, _f32, shape[:3]),
+            None if seq_lens is None else _expect(seq_lens, "seq_lens", dev, _i32, (B,)))
+    all_written = seq_lens is None and keep <= Nk
 
-        k_out = new(k_out, (B, Hkv, keep, d), dt, 0)
-        v_out = new(v_out, (B, Hkv, keep, d), dt, 0)
-        weights_out = new(weights_out, (B, Hkv, keep), f32, 0)
-        index_out = new(index_out, (B, Hkv, keep), torch.int32, -1)
-        _check(lib().fa_kv_evict(code, *ptrs, k_out.data_ptr(), v_out.data_ptr(), weights_out.data_ptr(),
-                                 index_out.data_ptr(), B, Hkv, Nk, d, keep, recent, _raw_stream(dev)))
+    def out(t, name, dtype, shape, fill):
+        if t is None:
+            t = k.new_empty(shape, dtype=dtype) if all_written else k.new_full(shape, fill, dtype=dtype)
+            return t, t.data_ptr()
+        return t, _expect(t, name, dev, dtype, shape)
+
+    with _on_device(stream, dev):
+        k_out, pk = out(k_out, "k_out", dt, (B, Hkv, keep, d), 0)
+        v_out, pv = out(v_out, "v_out", dt, (B, Hkv, keep, d), 0)
+        weights_out, pw = out(weights_out, "weights_out", _f32, (B, Hkv, keep), 0)
+        index_out, pi = out(index_out, "index_out", _i32, (B, Hkv, keep), -1)
+        _check(lib().fa_kv_evict(code, *ptrs, pk, pv, pw, pi, B, Hkv, Nk, d, keep, recent, _current_stream(dev)))
     return k_out, v_out, weights_out, index_out
 
 
