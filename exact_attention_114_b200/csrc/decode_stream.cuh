@@ -585,22 +585,22 @@ struct StreamParts {
     }
 };
 
-// Adds up to eight parts' rows at a time, their loads in flight together: part i has its row at
+// Adds up to AT_ONCE parts' rows at a time, their loads in flight together: part i has its row at
 // row_of(i) (of both o and lse), lane l columns 4 l .. 4 l + 3.  Returns the running (M, L, acc).
 struct MergeState {
     float M, L;
     float4 acc;
 };
 
-template <typename F>
+template <int AT_ONCE, typename F>
 __device__ __forceinline__ void merge_parts(MergeState& st, const float* o, const float* lse, int ld, int n, bool cols, F row_of)
 {
     const int lane = lane_id();
-    for (int i0 = 0; i0 < n; i0 += 8) {
-        float ls[8];
-        float4 v[8];
+    for (int i0 = 0; i0 < n; i0 += AT_ONCE) {
+        float ls[AT_ONCE];
+        float4 v[AT_ONCE];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < AT_ONCE; ++k) {
             ls[k] = -INFINITY;
             v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i0 + k < n) {
@@ -612,7 +612,7 @@ __device__ __forceinline__ void merge_parts(MergeState& st, const float* o, cons
         }
         float M = st.M;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < AT_ONCE; ++k)
             M = fmaxf(M, ls[k]);
         if (M == -INFINITY)
             continue;
@@ -624,7 +624,7 @@ __device__ __forceinline__ void merge_parts(MergeState& st, const float* o, cons
         st.acc.z *= a;
         st.acc.w *= a;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < AT_ONCE; ++k) {
             if (ls[k] == -INFINITY)   // no key there: its row may never have been written
                 continue;
             const float w = ex2_approx(ls[k] - M);
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(128) stream_combine_kernel(StreamParts p, void
     if (n == 1)
         return;
     MergeState st{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    merge_parts(st, p.o, p.lse, 128, n, lane * 4 < d_io, [&](int i) { return p.slot(unit, c0, n, i) * p.R + r; });
+    merge_parts<8>(st, p.o, p.lse, 128, n, lane * 4 < d_io, [&](int i) { return p.slot(unit, c0, n, i) * p.R + r; });
     merge_store(st, static_cast<T*>(o_out), lse_out, (size_t)row, d_io, lane * 4);
 }
 

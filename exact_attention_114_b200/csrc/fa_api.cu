@@ -527,8 +527,13 @@ fa_status_t launch_fwd_tiles(Kern kern, int threads, int smem, const CUtensorMap
     if (merge) {
         if (st == FA_OK) {
             const long long rows = (long long)p.n_bh * p.rows;
-            st = launch_dependent("fwd_combine_kernel launch", fa::fwd_combine_kernel<T>,
-                                  dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, p);
+            if constexpr (MODE == fa::kFwdPlain)
+                st = launch_dependent("fwd_combine_kernel launch", fa::fwd_combine_kernel<T>,
+                                      dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, p);
+            else
+                st = launch_dependent("share_merge_kernel launch",
+                                      p.kv_split <= 2 ? fa::share_merge_kernel<2, T> : fa::share_merge_kernel<4, T>,
+                                      dim3((unsigned)((rows * ((p.d_io + 127) / 128) + 3) / 4)), dim3(128), 0, stream, p);
         }
         cudaError_t e = cudaFreeAsync(ws, stream);
         if (e != cudaSuccess && st == FA_OK)
