@@ -41,6 +41,7 @@ struct StreamParams {
     int B, Hq, Hkv, Nq, Nk, G, R, d_io;
     int causal;
     int window, sinks;
+    int sink_rows;          // rows loaded of the last tile of sinks: sinks % 64 rounded up to 8, or 64
     int np;                 // prefix keys (kListCat)
     int page_size, max_pages;
     int partial;            // every unit as a partial
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(160, 2)
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
             const bool two = d_io > 64;   // the second 64-column panel only when the head has columns there
-            const uint32_t bytes = (uint32_t)(two ? 4 : 2) * DecCfg::kPanelBytes;
+            const uint32_t row_bytes = (two ? 4u : 2u) * 128u;   // a key's K and V in a stage
             int n = 0, units = 0;
             bool go = any;
             while (go) {
@@ -285,7 +286,10 @@ __global__ void __launch_bounds__(160, 2)
                         break;
                     uint8_t* dk = smem + slot * 2 * DecCfg::kTileBytes;
                     uint8_t* dv = dk + DecCfg::kTileBytes;
-                    mbar_arrive_expect_tx(&bar_full[slot], bytes + (t == t0 ? (uint32_t)q_bytes : 0u));
+                    // the last tile of sinks, where the window has no key in it: only the sinks' rows
+                    const bool few = (LIST == kListWindow || LIST == kListPaged) && t == at.l.seg - 1 && at.l.win_lo >= at.l.seg * kt;
+                    mbar_arrive_expect_tx(&bar_full[slot],
+                                          row_bytes * (uint32_t)(few ? p.sink_rows : kt) + (t == t0 ? (uint32_t)q_bytes : 0u));
                     if (t == t0) {
                         bulk_load(smem + C::kOffQ + (units % q_slots) * q_bytes,
                                   static_cast<const T*>(p.q) + (size_t)(at.b * p.Hkv + at.hk) * p.R * d_io, (uint32_t)q_bytes,
@@ -298,14 +302,16 @@ __global__ void __launch_bounds__(160, 2)
                         // an out-of-range page id reads zeros (TMA bounds), never another buffer
                         const int page = __ldg(p.block_table + (size_t)at.b * p.max_pages + key0 / p.page_size);
                         const int off = key0 % p.page_size;
+                        const CUtensorMap* mk = few ? &tmK0 : &tmK;
+                        const CUtensorMap* mv = few ? &tmV0 : &tmV;
                         for (int pn = 0; pn < (two ? 2 : 1); ++pn) {
-                            tma_load_4d(dk + pn * DecCfg::kPanelBytes, &tmK, &bar_full[slot], pn * 64, at.hk, off, page);
-                            tma_load_4d(dv + pn * DecCfg::kPanelBytes, &tmV, &bar_full[slot], pn * 64, at.hk, off, page);
+                            tma_load_4d(dk + pn * DecCfg::kPanelBytes, mk, &bar_full[slot], pn * 64, at.hk, off, page);
+                            tma_load_4d(dv + pn * DecCfg::kPanelBytes, mv, &bar_full[slot], pn * 64, at.hk, off, page);
                         }
                     } else {
                         const bool pre = LIST == kListCat && head_seg;
-                        const CUtensorMap* mk = pre ? &tmK0 : &tmK;
-                        const CUtensorMap* mv = pre ? &tmV0 : &tmV;
+                        const CUtensorMap* mk = pre || few ? &tmK0 : &tmK;
+                        const CUtensorMap* mv = pre || few ? &tmV0 : &tmV;
                         const int head = pre ? at.hk : at.b * p.Hkv + at.hk;
                         for (int pn = 0; pn < (two ? 2 : 1); ++pn) {
                             tma_load_3d(dk + pn * DecCfg::kPanelBytes, mk, &bar_full[slot], pn * 64, key0, head);
@@ -409,8 +415,8 @@ __global__ void __launch_bounds__(160, 2)
                     if (out)
                         s[nt][e] = -INFINITY;
                 }
-            // V of keys that no row sees (between the sinks and the window; past the sequence, in its
-            // last page or in the padding) is cleared in the operand registers: whatever is there,
+            // V of keys that no row sees (between the sinks and the window, where the stage may hold an
+            // older tile's rows; past the sequence, in its last page or in the padding) is cleared in the operand registers: whatever is there,
             // 0 * V adds nothing.  A thread's operand words hold keys 2 tq, 2 tq + 1 (keep[0]) and 8
             // further on (keep[1]) of the warp's 16.
             uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};

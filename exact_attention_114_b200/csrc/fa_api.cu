@@ -195,9 +195,9 @@ fa_status_t make_map_rows(CUtensorMap* m, const void* base, uint64_t inner, uint
 }
 
 // 4-D map over a paged KV pool [pages][page_size][Hkv][d] (bf16), box {64, 1, 64, 1}
-// (one kv head, 64 keys of one page), 128-byte swizzle.
+// (one kv head, 64 keys of one page, or box_rows of them), 128-byte swizzle.
 fa_status_t make_map_paged(CUtensorMap* m, const void* base, uint64_t d, uint64_t Hkv, uint64_t page_size,
-                           uint64_t pages, CUtensorMapDataType dt)
+                           uint64_t pages, CUtensorMapDataType dt, uint32_t box_rows = 64)
 {
     EncodeTiledFn enc = get_encode();
     if (!enc) {
@@ -206,7 +206,7 @@ fa_status_t make_map_paged(CUtensorMap* m, const void* base, uint64_t d, uint64_
     }
     cuuint64_t dims[4] = {d, Hkv, page_size, pages};
     cuuint64_t strides[3] = {d * 2, Hkv * d * 2, page_size * Hkv * d * 2};
-    cuuint32_t box[4] = {64, 1, 64, 1};
+    cuuint32_t box[4] = {64, 1, box_rows, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = enc(m, dt, 4, const_cast<void*>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1032,6 +1032,7 @@ fa::StreamParams stream_params(const StreamArgs& a)
     p.causal = a.causal;
     p.window = a.win.window;
     p.sinks = a.win.sinks;
+    p.sink_rows = a.win.sinks % 64 ? (a.win.sinks % 64 + 7) / 8 * 8 : 64;
     p.np = a.np;
     p.partial = a.partial;
     p.after = a.after;
@@ -1117,6 +1118,14 @@ fa_status_t launch_stream(const StreamArgs& a, const StreamPlan& pl, void* ws, c
     } else {
         mk0 = mk;
         mv0 = mv;
+        const uint32_t rows = (uint32_t)stream_params(a).sink_rows;
+        if (a.list == fa::kListPaged && rows < 64) {
+            if ((st = make_map_paged(&mk0, a.k, a.d, a.Hkv, a.pg->page_size, a.pg->num_pages, dt, rows)) != FA_OK) return st;
+            if ((st = make_map_paged(&mv0, a.v, a.d, a.Hkv, a.pg->page_size, a.pg->num_pages, dt, rows)) != FA_OK) return st;
+        } else if (a.list == fa::kListWindow && rows < 64) {
+            if ((st = make_map(&mk0, a.k, a.d, a.Nk, units, rows, dt)) != FA_OK) return st;
+            if ((st = make_map(&mv0, a.v, a.d, a.Nk, units, rows, dt)) != FA_OK) return st;
+        }
     }
     const bool narrow = a.d < 128;
     auto pick = [&](auto list, auto scores) {
