@@ -657,42 +657,71 @@ __device__ __forceinline__ void merge_store(const MergeState& st, T* o, float* l
 // One warp per row: the parts of units cut between CTAs; rows of units within one CTA are final,
 // and rows of a sequence without keys get O = 0, LSE = -inf.
 template <typename T>
-__global__ void __launch_bounds__(128) stream_combine_kernel(StreamParts p, void* o_out, float* lse_out, int d_io)
+__device__ __forceinline__ void stream_combine_rows(const StreamParts& p, T* o_out, float* lse_out, int d_io, int block)
 {
-    griddep_launch_dependents();
-    const int row = (int)(blockIdx.x * 4 + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const int unit = row / p.R, r = row % p.R;
-    griddep_wait();
+    const int row = block * 4 + (int)(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= p.B * p.Hkv * p.R)
         return;
+    const int unit = row / p.R, r = row % p.R;
     int c0;
     const int n = p.count(unit, c0);
     if (n == 1)
         return;
     MergeState st{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     merge_parts<8>(st, p.o, p.lse, 128, n, lane * 4 < d_io, [&](int i) { return p.slot(unit, c0, n, i) * p.R + r; });
-    merge_store(st, static_cast<T*>(o_out), lse_out, (size_t)row, d_io, lane * 4);
+    merge_store(st, o_out, lse_out, (size_t)row, d_io, lane * 4);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(128) stream_combine_kernel(StreamParts p, void* o_out, float* lse_out, int d_io)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    stream_combine_rows(p, static_cast<T*>(o_out), lse_out, d_io, (int)blockIdx.x);
 }
 
 // The weights that the keys receive, from the scores that the pass has left and the rows' LSE:
-// thread i takes four keys of a (batch, kv head).  Bound by reading the scores (mostly in L2).
+// thread i takes four keys of a (batch, kv head).  Bound by reading the scores (mostly in L2).  The
+// blocks after the keys' merge the units that are cut between CTAs, so that neither waits for the
+// other: a keys' block takes the LSE of such a unit from its parts.
 struct DecodeWeightParams {
     const float* scores;    // [BH, R, stride]: log2 units, -inf where masked
-    const float* lse;       // [BH, R]
+    float* lse;             // [BH, R]: final for units within one CTA, written by the merge for the others
     const float* w_in;      // [BH, Nk] or nullptr (zeros)
     float* w_out;
-    int BH, R, Nk, stride;
+    void* o;
+    int BH, R, Nk, stride, d_io;
+    int key_blocks;         // BH * ceil(Nk / 512)
+    StreamParts parts;
 };
 
+template <typename T>
 __global__ void __launch_bounds__(128) decode_weights_kernel(DecodeWeightParams p)
 {
     __shared__ float s_lse[16];
     griddep_wait();
+    if ((int)blockIdx.x >= p.key_blocks) {
+        stream_combine_rows(p.parts, static_cast<T*>(p.o), p.lse, p.d_io, (int)blockIdx.x - p.key_blocks);
+        return;
+    }
     const int chunks = (p.Nk + 511) / 512;
     const int bh = (int)blockIdx.x / chunks, key = ((int)blockIdx.x % chunks) * 512 + (int)threadIdx.x * 4;
     if ((int)threadIdx.x < p.R) {
-        const float l = p.lse[(size_t)bh * p.R + threadIdx.x];
-        s_lse[threadIdx.x] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;   // P = 0 in a row without keys
+        const int r = (int)threadIdx.x;
+        int c0;
+        const int n = p.parts.count(bh, c0);
+        float l;   // log2 units
+        if (n == 1) {
+            l = p.lse[(size_t)bh * p.R + r] * 1.4426950408889634f;
+        } else {
+            float M = -INFINITY, L = 0.f;
+            for (int i = 0; i < n; ++i)
+                M = fmaxf(M, p.parts.lse[p.parts.slot(bh, c0, n, i) * p.R + r]);
+            for (int i = 0; i < n && M != -INFINITY; ++i)
+                L += ex2_approx(p.parts.lse[p.parts.slot(bh, c0, n, i) * p.R + r] - M);
+            l = L > 0.f ? M + __log2f(L) : -INFINITY;
+        }
+        s_lse[r] = l == -INFINITY ? INFINITY : l;   // P = 0 in a row without keys
     }
     __syncthreads();
     if (key >= p.Nk)

@@ -1152,7 +1152,7 @@ fa_status_t launch_stream(const StreamArgs& a, const StreamPlan& pl, void* ws, c
         kern<<<(unsigned)pl.grid, C::kThreads, C::kSmemBytes, stream>>>(mk, mv, mk0, mv0, p);
         st = check_launch("decode_stream_kernel launch");
     }
-    if (st != FA_OK || a.partial || !pl.merge)
+    if (st != FA_OK || a.partial || a.scores || !pl.merge)   // with scores: merged beside the keys' weights
         return st;
     const long long rows = (long long)units * p.R;
     return launch_dependent("stream_combine_kernel launch", fa::stream_combine_kernel<T>, dim3((unsigned)((rows + 3) / 4)),
@@ -2472,13 +2472,19 @@ fa_status_t fa_fwd_weights(fa_dtype_t dtype, const void* q, const void* k, const
                 p.lse = a.lse;
                 p.w_in = weights_in;
                 p.w_out = weights_out;
+                p.o = o;
                 p.BH = B * Hkv;
                 p.R = Hq / Hkv * Nq;
                 p.Nk = Nk;
                 p.stride = a.score_stride;
-                const long long blocks = (long long)p.BH * ((Nk + 511) / 512);
-                st = launch_dependent("decode_weights_kernel launch", fa::decode_weights_kernel, dim3((unsigned)blocks),
-                                      dim3(128), 0, s, p);
+                p.d_io = d;
+                p.key_blocks = p.BH * ((Nk + 511) / 512);
+                p.parts = stream_parts(a, pl, ws);
+                const long long blocks = p.key_blocks + (pl.merge ? ((long long)p.BH * p.R + 3) / 4 : 0);
+                st = launch_dependent("decode_weights_kernel launch",
+                                      dtype == FA_DTYPE_FP16 ? fa::decode_weights_kernel<__half>
+                                                             : fa::decode_weights_kernel<__nv_bfloat16>,
+                                      dim3((unsigned)blocks), dim3(128), 0, s, p);
             }
         } else {
             float* l = lse;
