@@ -24,6 +24,13 @@
 // order and writes dK / dV.  The last waits only for CTAs that have finished their
 // steps, so the wait cannot depend on a CTA that is not yet running.
 //
+// Sliding window with sinks (WIN): a key block walks only the query blocks that see it, window +
+// 127 rows, except the blocks that hold sinks, which every later query sees.  With equal
+// shares those would run on after the others (at 8192 rows, window 1024, one sinks' unit is 6.5
+// others), so the launch has two parts, each with its own number of CTAs per unit.  Same
+// bound as the dense kernel (tensor and shared memory), over blocks of 1.2 times the visible
+// pairs: 460 us of the 525 us backward at that shape with 32 / 8 heads, d = 128.
+//
 // bwd_main roles (384 threads = 3 warpgroups):
 //   warps 0-3  thread r = key r = TMEM lane r: read S^T and dP^T rows from TMEM,
 //              write P^T (bf16) back over S^T in TMEM and dS^T (bf16) into

@@ -1367,8 +1367,8 @@ PrefixPlan prefix_plan(const PrefixArgs& a, int dtype)
     const size_t total_rows = (size_t)a.B * a.Hq * a.Nq;
     const int kt = kernel_d(a.d) == 256 ? 1 : 2;
     const int tiles = (a.B + pack - 1) / pack;
-    pl.shares = prefix_shares((long long)((tiles + kt - 1) / kt) * a.Hkv, (a.Np + 127) / 128, total_rows * a.d * 4.0,
-                              sm_count());
+    const long long units = (long long)((tiles + kt - 1) / kt) * a.Hkv;
+    pl.shares = prefix_shares(units, (a.Np + 127) / 128, total_rows * a.d * 4.0, sm_count());
     pl.a_lse = align256(total_rows * pl.shares * a.d * 4);
     pl.b_o = pl.a_lse + align256(total_rows * pl.shares * 4);
     if (pl.decode) {

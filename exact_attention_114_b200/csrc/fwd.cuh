@@ -47,6 +47,19 @@
 // fwd_combine_kernel merges the shares by their lse (the same rescale-and-add as
 // between blocks).
 //
+// Key lists (MODE): a tile may walk another list of key blocks than 0, 1, 2, ...
+//   * kFwdWindow (sliding window with sinks): the sinks, padded to whole 8-row
+//     swizzle atoms, then the keys from the first window key of the tile's first
+//     row.  The block where the two meet is two TMA boxes.  A window starts and
+//     ends inside a block for most rows, so the masks are visible columns as bits,
+//     and only for warps with a row that needs one (8192 rows, window 1024, 4 sinks,
+//     32 heads, d = 128: 174 us, 743 TFLOP/s over the visible pairs; compared
+//     element by element 274 us).  Bound by the tensor pipe and the exponentials,
+//     over blocks of 1.3 times the visible pairs.
+//   * kFwdCat (shared prefix): the prefix's blocks, then the sequence's own.
+//   * kFwdPack (shared prefix): the prefix's blocks for a tile that holds the rows of
+//     several sequences; always ends in partials.
+//
 // Scores are kept in the log2 domain: x = s * scale * log2(e), p = 2^(x - m).
 // Rescaling is lazy: the reference max m moves (and U, l are multiplied by
 // 2^(m_old - m_new)) only when the block max exceeds it by more than

@@ -17,7 +17,7 @@
  * --------------------------------
  *  - Tensors are dense, row-major, "BHSD": q, o, dout, dq are [B, Hq, Nq, d];
  *    k, v, dk, dv are [B, Hkv, Nk, d]; lse is [B, Hq, Nq].  q/k/v/o/dout/dq/dk/dv
- *    hold bf16 (fp16 through the *_ex calls), lse holds fp32 (natural log of
+ *    hold bf16 (fp16 through the *_ex calls and those with a dtype argument), lse holds fp32 (natural log of
  *    the scaled scores).
  *  - Every tensor pointer is a DEVICE pointer, non-NULL and 16-byte aligned.
  *  - d is a multiple of 32 up to 256 (page "AI infra 一层全看懂(五) Flash
@@ -36,8 +36,9 @@
  *    enqueued on it; no call synchronises the stream or the device.  A call's
  *    first kernel is a plain launch: it starts after all earlier work on the
  *    stream.  Its later kernels (the backward's main and post passes, the merge of
- *    split partials, the e4m3 forward after its V transpose) are programmatic
- *    dependent launches.  They may start their
+ *    split partials, the e4m3 forward after its V transpose, the own keys' pass of
+ *    fa_fwd_prefix, the additions of keys' weights, the gather of an eviction) are
+ *    programmatic dependent launches.  They may start their
  *    set-up while the kernel before them finishes, but they read nothing that
  *    kernel writes until it has completed.  Later work on the stream starts after
  *    the whole call, as usual.
@@ -119,7 +120,8 @@ const char* fa_last_error_message(void);
  * blocks (§04).  The blocks share a tile
  * counter, one of 256 slots in the library's device memory that launches take
  * in turn; the launch's last block resets it.  So at most 256 tiled forward
- * launches (this call, fa_fwd_ex, fa_fwd_fp8) may be in flight on one device
+ * launches (this call, fa_fwd_ex, fa_fwd_fp8, and the tiled launches of
+ * fa_fwd_window, fa_fwd_prefix and fa_fwd_weights) may be in flight on one device
  * at once.  Each launch marks its slot with a tag of its own; a launch whose
  * blocks find the slot held by another launch takes no tile from it, leaves
  * its own output incomplete and records FA_ERR_SLOT_CONFLICT in the device
