@@ -996,6 +996,19 @@ __global__ void __launch_bounds__(384, 1)
                         // this share's normalised partial O_s in fp32
                         if (row_valid) {
                             const size_t prow = part_row();
+                            if constexpr (MODE != kFwdPlain) {
+                                // whole 32-byte sectors (a row per lane: 16-byte stores touch each twice)
+                                float* d8 = p.part_o + prow * p.d_io + c0;
+#pragma unroll
+                                for (int c = 0; c < 32; c += 8) {
+                                    float x[8];
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e)
+                                        x[e] = __uint_as_float(o[c + e]) * inv_l;
+                                    st_global_v8(d8 + c, x);
+                                }
+                                continue;
+                            }
                             float4* dst = reinterpret_cast<float4*>(p.part_o + prow * p.d_io + c0);
 #pragma unroll
                             for (int c = 0; c < 8; ++c)

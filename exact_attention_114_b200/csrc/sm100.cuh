@@ -648,6 +648,14 @@ struct Elt<__half> {
     __device__ static __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
 };
 
+// 32-byte store (the address a multiple of 32).
+__device__ __forceinline__ void st_global_v8(float* dst, const float (&x)[8])
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
+
 // The low n bits (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t bits_below(int n)
 {
