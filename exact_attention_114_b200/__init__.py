@@ -463,6 +463,11 @@ def _scale(scale, d):
     return 1.0 / math.sqrt(d) if scale is None else float(scale)
 
 
+def _keys(n):
+    """A number of keys as the C call's int: more than any cache holds stays the largest (not a remainder)."""
+    return min(int(n), 0x7FFFFFFF)
+
+
 def _qkv(q, k, v):
     """Device, dtype code, element type, sizes and pointers of q, k and v."""
     code, dt, dev = _start(q, "q")
@@ -501,20 +506,20 @@ def fa_fwd_window(q, k, v, window, sinks=0, o=None, lse=None, *, scale=None, str
         pl = None
         if lse is not None or want_lse:
             lse, pl = _out_lse(lse, q, sizes, dev)
-        _check(lib().fa_fwd_window(code, *ptrs, po, pl, *sizes, _scale(scale, sizes[5]), int(window), int(sinks),
+        _check(lib().fa_fwd_window(code, *ptrs, po, pl, *sizes, _scale(scale, sizes[5]), _keys(window), _keys(sinks),
                                    _current_stream(dev)))
     return o, lse
 
 
 def fa_bwd_window_workspace_size(B, Hq, Hkv, Nq, Nk, d, window, sinks=0) -> int:
-    return int(lib().fa_bwd_window_workspace_size(B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks)))
+    return int(lib().fa_bwd_window_workspace_size(B, Hq, Hkv, Nq, Nk, d, _keys(window), _keys(sinks)))
 
 
 def fa_bwd_window_query_split(B, Hq, Hkv, Nq, Nk, d, window, sinks=0):
     """CTAs that share each unit of ``fa_bwd_window`` on the current device, given a full-size workspace:
     (of a key block without sinks, of one with sinks); 0 for bad sizes."""
     sink_split = ctypes.c_int(0)
-    split = lib().fa_bwd_window_query_split(B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks), ctypes.byref(sink_split))
+    split = lib().fa_bwd_window_query_split(B, Hq, Hkv, Nq, Nk, d, _keys(window), _keys(sinks), ctypes.byref(sink_split))
     return int(split), sink_split.value
 
 
@@ -530,14 +535,14 @@ def fa_bwd_window(q, k, v, o, dout, lse, window, sinks=0, dq=None, dk=None, dv=N
         dq, pq = _out(dq, "dq", q, dev, dt)
         dk, pk = _out(dk, "dk", k, dev, dt)
         dv, pv = _out(dv, "dv", k, dev, dt)
-        _check(lib().fa_bwd_window(code, *ptrs, pq, pk, pv, *sizes, _scale(scale, sizes[5]), int(window), int(sinks),
+        _check(lib().fa_bwd_window(code, *ptrs, pq, pk, pv, *sizes, _scale(scale, sizes[5]), _keys(window), _keys(sinks),
                                    *ws, _current_stream(dev)))
     return dq, dk, dv
 
 
 def fa_fwd_paged_window_workspace_size(B, Hq, Hkv, Nq, page_size, max_pages_per_seq, d, window, sinks=0) -> int:
     return int(lib().fa_fwd_paged_window_workspace_size(B, Hq, Hkv, Nq, page_size, max_pages_per_seq, d,
-                                                        int(window), int(sinks)))
+                                                        _keys(window), _keys(sinks)))
 
 
 def fa_fwd_paged_window(q, k_cache, v_cache, block_table, seq_lens, window, sinks=0, o=None, lse=None, *,
@@ -558,7 +563,7 @@ def fa_fwd_paged_window(q, k_cache, v_cache, block_table, seq_lens, window, sink
         o, po = _out(o, "o", q, dev, dt)
         lse, pl = _out_lse(lse, q, (B, Hq, Hkv, Nq), dev)
         _check(lib().fa_fwd_paged_window(code, *ptrs, po, pl, B, Hq, Hkv, Nq, d, page_size, num_pages,
-                                         block_table.shape[1], _scale(scale, d), int(window), int(sinks), *ws,
+                                         block_table.shape[1], _scale(scale, d), _keys(window), _keys(sinks), *ws,
                                          _current_stream(dev)))
     return o, lse
 

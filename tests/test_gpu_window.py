@@ -279,6 +279,33 @@ def test_whole_window_is_causal_attention():
     o, lse = fa.fa_fwd_window(q, k, v, 640)
     o1, l1 = fa.fa_fwd(q, k, v, causal=True)
     assert torch.equal(o, o1) and torch.equal(lse, l1)
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 40, 0), (1, 2 ** 32 + 640)):   # larger than an int: no remainder
+        o2, l2 = fa.fa_fwd_window(q, k, v, window, sinks)
+        r = ref_of(q, k, v, 640, 640)
+        close(o2, r.o, r.o_tol, "o")
+        close(l2, r.lse, r.lse_tol, "lse")
+
+
+def test_other_stream_and_given_outputs():
+    """On a stream that is not current, into outputs of the caller, with a scale of its own."""
+    q, k, v, dout = make(2, 4, 2, 150, 400, 96, FP16, 1050)
+    s = torch.cuda.Stream()
+    o, lse = torch.full_like(q, 9), torch.full(q.shape[:3], 9.0, device="cuda")
+    grads = [torch.full_like(t, 9) for t in (q, k, v)]
+    s.wait_stream(torch.cuda.current_stream())
+    assert fa.fa_fwd_window(q, k, v, 70, 6, o, lse, scale=0.2, stream=s)[0] is o
+    fa.fa_bwd_window(q, k, v, o, dout, lse, 70, 6, *grads, scale=0.2, stream=s)
+    s.synchronize()
+    seen = window_seen(150, 400, 70, 6, q.device).repeat(2, 1)
+    r = Ref(grouped(q, 2), k, v, seen, scale=0.2, dout=grouped(dout, 2))
+    close(o, r.o, r.o_tol, "o")
+    close(lse, r.lse, r.lse_tol, "lse")
+    for got, ref, tol in zip(grads, (r.dq, r.dk, r.dv), (r.dq_tol, r.dk_tol, r.dv_tol)):
+        close(got, ref, tol, "gradient")
+    with pytest.raises(ValueError):
+        fa.fa_fwd_window(q, k.transpose(2, 3).contiguous().transpose(2, 3), v, 70)   # not contiguous
+    with pytest.raises(ValueError):
+        fa.fa_fwd_window(q, k, v, 70, o=o.bfloat16())
 
 
 def test_graph_and_streams():
