@@ -674,6 +674,46 @@ fa_status_t check_window(int window, int sinks, int Nk, Window* w)
     return FA_OK;
 }
 
+// Two shares of every work tile as a cluster of two CTAs (no partials through memory): where that
+// takes no more CTAs than SMs and less time than the plan `sp` of shares merged by a kernel.  In block
+// times of the longest tile, plus 3 for the plan's merge kernel and 1.5 for a pair's exchange (as
+// measured: 512 rows on 16K keys 53.9 us merged by the kernel, 47.6 as pairs; 40 rows on 5K keys, whose
+// 2 tiles take 8 shares each, 18.9 against 26.7).
+bool fwd_pairs(const FwdGeom& g, int tiles_per_cta, int longest, const FwdSplit& sp, int sms)
+{
+    const long long units = (long long)g.n_pairs * g.n_bh;
+    if (tiles_per_cta != 2 || longest < 3 || 2 * units > sms)
+        return false;
+    const double plan = (double)((longest + sp.shares - 1) / sp.shares) + (sp.shares > 1 ? 3.0 : 0.0);
+    return (double)((longest + 1) / 2) + 1.5 < plan;
+}
+
+template <typename Kern, typename E>
+fa_status_t launch_fwd_pairs(Kern kern, int threads, int smem, const CUtensorMap& mq, const CUtensorMap& mk,
+                             const CUtensorMap& mv, fa::FwdParams& p, cudaStream_t stream, const E& ex)
+{
+    p.kv_split = 2;
+    p.full_tiles = 0;
+    fa_status_t st;
+    if ((st = ensure_smem(reinterpret_cast<const void*>(kern), smem)) != FA_OK) return st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * p.n_pairs * p.n_bh));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, ex, p);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "fwd_kernel launch (pairs)");
+    return check_launch("fwd_kernel launch (pairs)");
+}
+
 template <int D, typename T>
 fa_status_t launch_fwd_win(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
                            int Nq, int Nk, int d, float scale, const Window& w, cudaStream_t stream)
@@ -714,6 +754,17 @@ fa_status_t launch_fwd_win(const void* q, const void* k, const void* v, void* o,
     p.sink_rem = rem;
     if ((st = fwd_tile_counter(&p.tile_ctr, &p.tile_tag)) != FA_OK)
         return st;
+    if constexpr (C::kTiles == 2) {
+        int longest = 0;
+        for (int pr = 0; pr < g.n_pairs && 2LL * g.n_pairs * g.n_bh <= sm_count(); ++pr) {
+            int lo, nb[2];
+            fa::fwd_win_blocks(pr * 256, 2, g.rows, Nq, Nk, w.window, w.sinks, 128 * full + rem, lo, nb);
+            longest = std::max(longest, std::max(nb[0], nb[1]));
+        }
+        if (fwd_pairs(g, C::kTiles, longest, sp, sm_count()))
+            return launch_fwd_pairs(fa::fwd_kernel<D, true, T, false, true, fa::kFwdWindow, true>, C::kThreads, C::kSmemBytes,
+                                    mq, mk, mv, p, stream, ex);
+    }
     return launch_fwd_tiles<T, fa::kFwdWindow>(kern, C::kThreads, C::kSmemBytes, mq, mk, mv, p, stream, false, ex);
 }
 
@@ -1293,6 +1344,11 @@ fa_status_t launch_prefix_cat(const PrefixArgs& a, int np, float* part_o, float*
     p.part_lse = part_lse;
     if ((st = fwd_tile_counter(&p.tile_ctr, &p.tile_tag)) != FA_OK)
         return st;
+    if constexpr (C::kTiles == 2) {
+        if (!part_o && fwd_pairs(g, C::kTiles, blocks, sp, sm_count()))
+            return launch_fwd_pairs(fa::fwd_kernel<D, true, T, false, true, fa::kFwdCat, true>, C::kThreads, C::kSmemBytes,
+                                    mq, mk, mv, p, stream, ex);
+    }
     return launch_fwd_tiles<T, fa::kFwdCat>(kern, C::kThreads, C::kSmemBytes, mq, mk, mv, p, stream, false, ex);
 }
 

@@ -60,6 +60,12 @@
 //   * kFwdPack (shared prefix): the prefix's blocks for a tile that holds the rows of
 //     several sequences; always ends in partials.
 //
+// Pairs (PAIR, for kFwdWindow and kFwdCat): where two shares of every work tile fill at most the
+// SMs, the two are a cluster of two CTAs, and no partial goes through memory.  Once both
+// have ended, the CTA of rank r takes query tile r: it gets the other's fp32 partial of that
+// tile through distributed shared memory (into its K/V ring, free by then), merges the two by
+// their lse and writes o.
+//
 // Scores are kept in the log2 domain: x = s * scale * log2(e), p = 2^(x - m).
 // Rescaling is lazy: the reference max m moves (and U, l are multiplied by
 // 2^(m_old - m_new)) only when the block max exceeds it by more than
@@ -297,13 +303,15 @@ __device__ __forceinline__ int fwd_take_tile(uint64_t* bar_tfull, uint64_t* bar_
 // without it the kernel carries none of the split's code.  MODE: the tile's list of key
 // blocks (kFwdWindow, kFwdPack, kFwdCat); only the list, its loads and its masks differ, and
 // for kFwdPack the rows of a tile.
-template <int D, bool CAUSAL, typename T = __nv_bfloat16, bool F8 = false, bool SPLIT = false, int MODE = kFwdPlain>
+template <int D, bool CAUSAL, typename T = __nv_bfloat16, bool F8 = false, bool SPLIT = false, int MODE = kFwdPlain,
+          bool PAIR = false>
 __global__ void __launch_bounds__(384, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdExtra<MODE> ex, FwdParams p)
 {
     static_assert(MODE == kFwdPlain || (CAUSAL && !F8), "other key lists: 16-bit inputs, one instance for both masks");
     using C = FwdCfg<D, F8>;
+    static_assert(!PAIR || (SPLIT && MODE != kFwdPlain && C::kTiles == 2), "pairs: two shares of two query tiles");
     griddep_launch_dependents();   // the merge of a key split may be scheduled
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -752,6 +760,11 @@ __global__ void __launch_bounds__(384, 1)
             }
         }
       }
+      if constexpr (PAIR) {
+          __syncwarp();
+          cluster_sync();   // both CTAs have ended
+          cluster_sync();   // the partials are in place
+      }
     } else {
         regs_inc<C::kRegsSoftmax>();
         // ------------------------------------------------------------ softmax
@@ -765,6 +778,7 @@ __global__ void __launch_bounds__(384, 1)
         int no = 0;   // earlier tiles with at least one block (bar_o phases)
         int su[2] = {0, 0};   // one-tile blocks: blocks of earlier tiles in S buffer 0 / 1
         bool ok = true;
+        bool paired = false;  // (PAIR: both cluster barriers passed)
 
         for (int u = 0; ok; ++u) {
             const int tile = fwd_take_tile(bar_tfull, bar_tfree, tile_ring, u, lane, abort_flag, ok);
@@ -980,6 +994,78 @@ __global__ void __launch_bounds__(384, 1)
                     return (size_t)w.share * (size_t)p.total_rows + (size_t)flat;
                 return ((size_t)w.bh * p.kv_split + w.share) * p.rows + qi;
             };
+            if constexpr (PAIR) {
+                if (nb > 0) {
+                    ok = mbar_wait(&bar_o[t], 0, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                }
+                const uint32_t rank = ctaid_x() & 1u;   // the share
+                const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
+                const float my_lse = (l > 0.f) ? m_ref + __log2f(l) : -INFINITY;
+                // the other's partial of this CTA's query tile: [D / 4][128 rows] of 4 columns, then lse
+                const uint32_t recv = smem_u32(sKV), recv_lse = recv + 128u * D * 4u;
+                cluster_sync();   // every P.V of both CTAs is done: their K/V rings are free
+                if ((uint32_t)t != rank) {
+                    const uint32_t to = cluster_smem(recv, rank ^ 1u), to_lse = cluster_smem(recv_lse, rank ^ 1u);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < p.d_io && nb > 0; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + (uint32_t)c0, o);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            st_cluster_f4(to + (uint32_t)(((c0 >> 2) + c) * 128 + r) * 16u,
+                                          make_float4(__uint_as_float(o[4 * c]) * inv_l, __uint_as_float(o[4 * c + 1]) * inv_l,
+                                                      __uint_as_float(o[4 * c + 2]) * inv_l, __uint_as_float(o[4 * c + 3]) * inv_l));
+                    }
+                    st_cluster_f1(to_lse + (uint32_t)r * 4u, my_lse);
+                }
+                cluster_sync();   // the partials are in place
+                paired = true;
+                if ((uint32_t)t == rank) {
+                    const float other = *reinterpret_cast<const float*>(sKV + 128 * D * 4 + r * 4);
+                    const float M = fmaxf(my_lse, other);
+                    const float w0 = my_lse == -INFINITY ? 0.f : ex2_approx(my_lse - M);
+                    const float w1 = other == -INFINITY ? 0.f : ex2_approx(other - M);
+                    const float L = w0 + w1, inv = (L > 0.f) ? 1.f / L : 0.f;
+                    const float a = w0 * inv * inv_l, b = w1 * inv;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < p.d_io; c0 += 32) {
+                        uint32_t o[32];
+                        if (nb > 0) {
+                            tmem_ld32(tO + (uint32_t)c0, o);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                o[c] = 0u;
+                        }
+                        uint32_t wv[16];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            // a share without keys wrote nothing
+                            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (w1 > 0.f)
+                                x = *reinterpret_cast<const float4*>(sKV + (((c0 >> 2) + c) * 128 + r) * 16);
+                            wv[2 * c] = Elt<T>::pack(fmaf(x.x, b, __uint_as_float(o[4 * c]) * a),
+                                                     fmaf(x.y, b, __uint_as_float(o[4 * c + 1]) * a));
+                            wv[2 * c + 1] = Elt<T>::pack(fmaf(x.z, b, __uint_as_float(o[4 * c + 2]) * a),
+                                                         fmaf(x.w, b, __uint_as_float(o[4 * c + 3]) * a));
+                        }
+                        if (row_valid) {
+                            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + row * p.d_io + c0);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                dst[c] = make_uint4(wv[4 * c], wv[4 * c + 1], wv[4 * c + 2], wv[4 * c + 3]);
+                        }
+                    }
+                    if (row_valid && p.lse)
+                        p.lse[row] = (L > 0.f) ? (M + __log2f(L)) * kLn2 : -INFINITY;
+                }
+                bt += nb;
+                continue;
+            }
             if (nb > 0) {
                 ok = mbar_wait(&bar_o[t], (uint32_t)(no & 1), abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
@@ -1054,6 +1140,11 @@ __global__ void __launch_bounds__(384, 1)
             bt += nb;
             su[0] += (nb + 1) / 2;
             su[1] += nb / 2;
+        }
+        if (PAIR && !paired) {   // gave up: the others still wait
+            __syncwarp();
+            cluster_sync();
+            cluster_sync();
         }
     }
 

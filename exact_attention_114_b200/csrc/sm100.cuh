@@ -648,6 +648,28 @@ struct Elt<__half> {
     __device__ static __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
 };
 
+// Cluster barrier (every thread of the cluster's CTAs; whole warps) and stores into another CTA's
+// shared memory.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_smem(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float4 x)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
+                 : "memory");
+}
+__device__ __forceinline__ void st_cluster_f1(uint32_t addr, float x)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+
 // 32-byte store (the address a multiple of 32).
 __device__ __forceinline__ void st_global_v8(float* dst, const float (&x)[8])
 {
