@@ -328,8 +328,9 @@ fa_status_t fa_bwd_ex(fa_dtype_t dtype, const void* q, const void* k, const void
  * causal = 1).  Only the key blocks that hold a visible key are read.  Keys that
  * no query row of the call sees may hold anything, NaN included.
  * Arguments, kernels and scratch otherwise as fa_fwd_ex (causal = 1): decode
- * shapes run the split-KV kernels, others the tiled one with its group rows and
- * key split.  The pages describe neither; they are the usual way to bound the
+ * shapes run a split-KV kernel, others the tiled one with its group rows and key
+ * split (or, where two shares of each tile fit the SMs, clusters of two blocks
+ * that merge them on chip: nothing is allocated then).  The pages describe neither; they are the usual way to bound the
  * cost of §04's recurrence for long histories.
  */
 fa_status_t fa_fwd_window(fa_dtype_t dtype, const void* q, const void* k, const void* v, void* o, float* lse,
