@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(EvictPar
     __shared__ int s_hist[kEvictBins];
     __shared__ int s_warp[32], s_eq[32];
     __shared__ uint32_t s_digit;
-    __shared__ int s_left, s_listed;
+    __shared__ int s_left, s_count, s_listed;
     griddep_launch_dependents();
     const int row = (int)blockIdx.x, tid = (int)threadIdx.x, warp = warp_id(), lane = lane_id();
     const int n = p.seq_lens ? max(0, min(__ldg(p.seq_lens + row / p.Hkv), p.Nk)) : p.Nk;
@@ -458,7 +458,8 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(EvictPar
                 atomicAdd(&s_hist[digit], 1);
             }
         };
-        // the bin, from the highest, in which `left` keys are reached; two bins per thread
+        // the bin, from the highest, in which `left` keys are reached, and its count (s_count: the
+        // histogram itself may be cleared by another thread once this returns); two bins per thread
         auto find = [&]() {
             __syncthreads();
             const int hi = kEvictBins - 1 - 2 * tid, a = s_hist[hi], b = s_hist[hi - 1];
@@ -466,9 +467,11 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(EvictPar
             if (before < left && left <= before + a) {
                 s_digit = (uint32_t)hi;
                 s_left = left - before;
+                s_count = a;
             } else if (before + a < left && left <= before + a + b) {
                 s_digit = (uint32_t)(hi - 1);
                 s_left = left - before - a;
+                s_count = b;
             }
             __syncthreads();
             left = s_left;
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_select_kernel(EvictPar
         if (need > 0) {
             left = need;
             T = find() << 21;
-            const int in_bin = s_hist[T >> 21];
+            const int in_bin = s_count;   // the same for all threads: written again only after the next barriers
             const bool listed = in_bin <= kEvictList;
             if (listed) {
                 for (int i0 = 0; i0 < m; i0 += kAtOnce * kEvictThreads) {

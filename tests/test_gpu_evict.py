@@ -122,6 +122,34 @@ def test_evict(case, kind):
     assert (index[:, :, n:] == -1).all() and not ko[:, :, n:].any() and not wo[:, :, n:].any()
 
 
+MANY = {
+    # weights of 20000 keys of which more than 8192 share sign, exponent and two bits of the mantissa
+    "equal": lambda w: torch.full_like(w, 0.25), "zeros": torch.zeros_like, "two": lambda w: torch.where(w < 0.4, 0.25, 0.26),
+    "close": lambda w: 1.0 + 0.2 * w, "signs": lambda w: torch.where(w < 0.5, -1.0, -1.1),
+}
+
+
+@pytest.mark.parametrize("kind", MANY)
+@pytest.mark.parametrize("keep,recent", [(6000, 100), (19999, 0)])
+def test_evict_many_alike(kind, keep, recent):
+    """More keys alike in the first digit than the list holds, while all are held in shared memory; a block per
+    (batch, kv head) on many SMs at once, repeated: every run selects the same."""
+    B, Hkv, Nk, d = 4, 40, 20000, 32
+    _, k, v, _ = make(B, 1, Hkv, 1, Nk, d, BF16, 2250)
+    w = MANY[kind](torch.rand((B, Hkv, Nk), generator=torch.Generator().manual_seed(2251)))
+    wg = w.cuda()
+    runs = [fa.fa_kv_evict(k, v, wg, keep, recent) for _ in range(8)]
+    torch.cuda.synchronize()
+    order = w.double()
+    order[..., Nk - recent:] = math.inf
+    want = torch.sort(order, dim=-1, descending=True, stable=True).indices[..., :keep].sort(-1).values
+    rows = want.cuda().unsqueeze(-1).expand(-1, -1, -1, d)
+    for ko, vo, wo, index in runs:
+        assert torch.equal(index.cpu().long(), want)
+        assert torch.equal(ko, torch.gather(k, 2, rows)) and torch.equal(vo, torch.gather(v, 2, rows))
+        assert torch.equal(wo.cpu(), torch.gather(w, 2, want))
+
+
 @pytest.mark.parametrize("keep,recent", [(50, 10), (1, 1), (200, 0)])
 def test_evict_lengths_and_rows_left_alone(keep, recent):
     """Sequences of their own lengths (none, one, the budget, one more, all): rows behind the last kept key stay."""
