@@ -1161,7 +1161,10 @@ __global__ void __launch_bounds__(384, 1)
 // LSE = (M + log2 sum_s w_s) ln 2 -- the rescale-and-add of the online softmax
 // (page "FlashAttention：为什么少搬数据，反而算得更快", §04) applied to whole
 // shares.  Shares with lse_s = -inf (no key) are skipped; a row no share sees
-// gets O = 0 and LSE = -inf.
+// gets O = 0 and LSE = -inf.  Bound by the latency of the shares' loads, so four
+// shares' are in flight (whole calls, four against one after another: 128 rows on
+// 8192 keys, 8 heads, d = 256, 28.5 to 24.9 us; 40 rows on 5000 keys, d = 64, 19.5
+// to 16.3; two shares of 512 rows on 16384 keys, 32 heads, unchanged).
 template <typename T = __nv_bfloat16>
 __global__ void __launch_bounds__(128) fwd_combine_kernel(FwdParams p)
 {
@@ -1195,33 +1198,45 @@ __global__ void __launch_bounds__(128) fwd_combine_kernel(FwdParams p)
         acc[k] = 0.f;
     const float* o0 = p.part_o + (((size_t)bh * ns) * p.rows + i) * p.d_io + (size_t)n * lane;
     const size_t share_stride = (size_t)p.rows * p.d_io;
-#pragma unroll 4
-    for (int s = 0; s < ns; ++s) {
-        const float w = __shfl_sync(0xffffffffu, wl, s);
-        if (w == 0.f)   // no key in this share (its O_s was never written) or a negligible one
-            continue;
-        const float* os = o0 + (size_t)s * share_stride;
-        if (n == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(os);
-            acc[0] = fmaf(w, v.x, acc[0]);
-            acc[1] = fmaf(w, v.y, acc[1]);
-            acc[2] = fmaf(w, v.z, acc[2]);
-            acc[3] = fmaf(w, v.w, acc[3]);
-        } else if (n == 8) {
-            const float4 v = *reinterpret_cast<const float4*>(os), u = *reinterpret_cast<const float4*>(os + 4);
-            acc[0] = fmaf(w, v.x, acc[0]);
-            acc[1] = fmaf(w, v.y, acc[1]);
-            acc[2] = fmaf(w, v.z, acc[2]);
-            acc[3] = fmaf(w, v.w, acc[3]);
-            acc[4] = fmaf(w, u.x, acc[4]);
-            acc[5] = fmaf(w, u.y, acc[5]);
-            acc[6] = fmaf(w, u.z, acc[6]);
-            acc[7] = fmaf(w, u.w, acc[7]);
-        } else {
+    // the loads of four shares are in flight together, and added in share order.  Shares of weight 0 are
+    // not read: no key (their O_s was never written) or a negligible weight
+    constexpr int kAtOnce = 4;
+    for (int s0 = 0; s0 < ns; s0 += kAtOnce) {
+        float w[kAtOnce], v[kAtOnce][8];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            w[j] = __shfl_sync(0xffffffffu, wl, s0 + j);   // (lanes from ns on hold 0)
+            const float* os = o0 + (size_t)(s0 + j) * share_stride;
+            if (w[j] == 0.f)
+                continue;
+            if (n == 4 || n == 8) {
+                const float4 x = *reinterpret_cast<const float4*>(os);
+                v[j][0] = x.x;
+                v[j][1] = x.y;
+                v[j][2] = x.z;
+                v[j][3] = x.w;
+                if (n == 8) {
+                    const float4 y = *reinterpret_cast<const float4*>(os + 4);
+                    v[j][4] = y.x;
+                    v[j][5] = y.y;
+                    v[j][6] = y.z;
+                    v[j][7] = y.w;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < n)
+                        v[j][k] = os[k];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            if (w[j] == 0.f)
+                continue;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 if (k < n)
-                    acc[k] = fmaf(w, os[k], acc[k]);
+                    acc[k] = fmaf(w[j], v[j][k], acc[k]);
         }
     }
     const float inv = (L > 0.f) ? 1.f / L : 0.f;
