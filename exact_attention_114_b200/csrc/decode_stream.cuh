@@ -540,8 +540,9 @@ __global__ void __launch_bounds__(160, 2)
                 acc.z = fmaf(x.z, sc, acc.z);
                 acc.w = fmaf(x.w, sc, acc.w);
             }
-            const float inv = (L > 0.f) ? __frcp_rn(L) : 0.f;
-            const float lse = (L > 0.f) ? M + __log2f(L) : -INFINITY;
+            // 0 and -inf only for a row without keys; a NaN L stays one, in a partial too
+            const float inv = L == 0.f ? 0.f : __frcp_rn(L);
+            const float lse = L == 0.f ? -INFINITY : M + __log2f(L);
             if (whole && !p.partial) {
                 const size_t row = (size_t)unit * p.R + r;
                 if (col < d_io)
@@ -595,7 +596,8 @@ struct StreamParts {
 };
 
 // Adds up to AT_ONCE parts' rows at a time, their loads in flight together: part i has its row at
-// row_of(i) (of both o and lse), lane l columns 4 l .. 4 l + 3.  Returns the running (M, L, acc).
+// row_of(i) (of both o and lse), lane l columns 4 l .. 4 l + 3.  Returns the running (M, L, acc).  A part
+// whose lse is NaN makes L NaN (M leaves it out).
 struct MergeState {
     float M, L;
     float4 acc;
@@ -623,9 +625,8 @@ __device__ __forceinline__ void merge_parts(MergeState& st, const float* o, cons
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k)
             M = fmaxf(M, ls[k]);
-        if (M == -INFINITY)
-            continue;
-        const float a = ex2_approx(st.M - M);
+        const float base = M == -INFINITY ? 0.f : M;   // no part with a number yet
+        const float a = ex2_approx(st.M - base);
         st.M = M;
         st.L *= a;
         st.acc.x *= a;
@@ -636,7 +637,7 @@ __device__ __forceinline__ void merge_parts(MergeState& st, const float* o, cons
         for (int k = 0; k < AT_ONCE; ++k) {
             if (ls[k] == -INFINITY)   // no key there: its row may never have been written
                 continue;
-            const float w = ex2_approx(ls[k] - M);
+            const float w = ex2_approx(ls[k] - base);
             st.L += w;
             st.acc.x = fmaf(w, v[k].x, st.acc.x);
             st.acc.y = fmaf(w, v[k].y, st.acc.y);
@@ -649,12 +650,12 @@ __device__ __forceinline__ void merge_parts(MergeState& st, const float* o, cons
 template <typename T>
 __device__ __forceinline__ void merge_store(const MergeState& st, T* o, float* lse, size_t row, int d_io, int col)
 {
-    const float inv = (st.L > 0.f) ? 1.f / st.L : 0.f;
+    const float inv = st.L == 0.f ? 0.f : 1.f / st.L;
     if (col < d_io)
         *reinterpret_cast<uint2*>(o + row * d_io + col) = make_uint2(Elt<T>::pack(st.acc.x * inv, st.acc.y * inv),
                                                                     Elt<T>::pack(st.acc.z * inv, st.acc.w * inv));
     if (col == 0 && lse)
-        lse[row] = (st.L > 0.f) ? (st.M + __log2f(st.L)) * 0.69314718055994530942f : -INFINITY;
+        lse[row] = st.L == 0.f ? -INFINITY : (st.M + __log2f(st.L)) * 0.69314718055994530942f;
 }
 
 // One warp per row: the parts of units cut between CTAs; rows of units within one CTA are final,
@@ -720,9 +721,10 @@ __global__ void __launch_bounds__(128) decode_weights_kernel(DecodeWeightParams 
             float M = -INFINITY, L = 0.f;
             for (int i = 0; i < n; ++i)
                 M = fmaxf(M, p.parts.lse[p.parts.slot(bh, c0, n, i) * p.R + r]);
-            for (int i = 0; i < n && M != -INFINITY; ++i)
-                L += ex2_approx(p.parts.lse[p.parts.slot(bh, c0, n, i) * p.R + r] - M);
-            l = L > 0.f ? M + __log2f(L) : -INFINITY;
+            const float base = M == -INFINITY ? 0.f : M;
+            for (int i = 0; i < n; ++i)
+                L += ex2_approx(p.parts.lse[p.parts.slot(bh, c0, n, i) * p.R + r] - base);
+            l = L == 0.f ? -INFINITY : M + __log2f(L);
         }
         s_lse[r] = l == -INFINITY ? INFINITY : l;   // P = 0 in a row without keys
     }
@@ -735,10 +737,11 @@ __global__ void __launch_bounds__(128) decode_weights_kernel(DecodeWeightParams 
     for (int r = 0; r < p.R; ++r) {
         const float4 x = *reinterpret_cast<const float4*>(sc + (size_t)r * p.stride);
         const float l = s_lse[r];
-        sum.x += ex2_approx(x.x - l);
-        sum.y += ex2_approx(x.y - l);
-        sum.z += ex2_approx(x.z - l);
-        sum.w += ex2_approx(x.w - l);
+        // a masked key gets nothing, of a row whose LSE is NaN neither
+        sum.x += x.x == -INFINITY ? 0.f : ex2_approx(x.x - l);
+        sum.y += x.y == -INFINITY ? 0.f : ex2_approx(x.y - l);
+        sum.z += x.z == -INFINITY ? 0.f : ex2_approx(x.z - l);
+        sum.w += x.w == -INFINITY ? 0.f : ex2_approx(x.w - l);
     }
     const float v[4] = {sum.x, sum.y, sum.z, sum.w};
     const size_t at = (size_t)bh * p.Nk + key;

@@ -876,17 +876,18 @@ __global__ void __launch_bounds__(384, 1)
                         if (kb + c > lim)
                             s[c] = -INFINITY;
                 }
-                // row max: two independent chains of three-input max
-                float mxa = fmaxf(s[0], s[1]), mxb = fmaxf(s[2], s[3]);
+                // row max: two independent chains of three-input max; NaN where a score is NaN
+                float mxa = fmax_nan(s[0], s[1]), mxb = fmax_nan(s[2], s[3]);
 #pragma unroll
                 for (int c = 4; c < 128; c += 4) {
-                    mxa = fmax3(mxa, s[c], s[c + 1]);
-                    mxb = fmax3(mxb, s[c + 2], s[c + 3]);
+                    mxa = fmax3_nan(mxa, s[c], s[c + 1]);
+                    mxb = fmax3_nan(mxb, s[c + 2], s[c + 3]);
                 }
-                const float m_blk = fmaxf(mxa, mxb) * sl2;
+                const float m_blk = fmax_nan(mxa, mxb) * sl2;
                 float a = 1.f;
                 bool resc = false;
-                if (m_blk > m_ref + kRescaleLog2) {
+                // (a NaN block is taken too: it makes l and O NaN, and so do the blocks after a NaN reference)
+                if (!(m_blk <= m_ref + kRescaleLog2)) {
                     a = ex2_approx(m_ref - m_blk);
                     resc = (j > 0);
                     m_ref = m_blk;
@@ -984,7 +985,13 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok)
                 break;
 
-            // ---- epilogue: O = U / l (bf16), LSE = (m + log2 l) ln 2
+            // an infinite reference: scores of +inf make the row NaN (inf - inf, which the software exp2 clamps),
+            // and where all are -inf none has any weight (that exp2 leaves 2^-125)
+            if (fabsf(m_ref) == INFINITY)
+                l *= m_ref > 0.f ? NAN : 0.f;
+
+            // ---- epilogue: O = U / l (bf16), LSE = (m + log2 l) ln 2; 0 and -inf only for l = 0 (no key with
+            // any weight), NaN for a NaN l
             const bool row_valid = (C::kTiles == 2 || t == 0) && qi < p.rows && in_pack;   // one-tile blocks: warps 4-7 idle
             const size_t row = (size_t)w.bh * (size_t)p.rows + (size_t)qi;   // the same flat row either way
             const bool partial = SPLIT && (w.nshares > 1 || MODE == kFwdPack || (MODE == kFwdCat && p.partial));
@@ -1003,8 +1010,8 @@ __global__ void __launch_bounds__(384, 1)
                     tc_fence_after();
                 }
                 const uint32_t rank = ctaid_x() & 1u;   // the share
-                const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
-                const float my_lse = (l > 0.f) ? m_ref + __log2f(l) : -INFINITY;
+                const float inv_l = l == 0.f ? 0.f : 1.f / l;
+                const float my_lse = l == 0.f ? -INFINITY : m_ref + __log2f(l);
                 // the other's partial of this CTA's query tile: [D / 4][128 rows] of 4 columns, then lse
                 const uint32_t recv = smem_u32(sKV), recv_lse = recv + 128u * D * 4u;
                 cluster_sync();   // every P.V of both CTAs is done: their K/V rings are free
@@ -1029,7 +1036,7 @@ __global__ void __launch_bounds__(384, 1)
                     const float M = fmaxf(my_lse, other);
                     const float w0 = my_lse == -INFINITY ? 0.f : ex2_approx(my_lse - M);
                     const float w1 = other == -INFINITY ? 0.f : ex2_approx(other - M);
-                    const float L = w0 + w1, inv = (L > 0.f) ? 1.f / L : 0.f;
+                    const float L = w0 + w1, inv = L == 0.f ? 0.f : 1.f / L;
                     const float a = w0 * inv * inv_l, b = w1 * inv;
 #pragma unroll 1
                     for (int c0 = 0; c0 < p.d_io; c0 += 32) {
@@ -1061,7 +1068,7 @@ __global__ void __launch_bounds__(384, 1)
                         }
                     }
                     if (row_valid && p.lse)
-                        p.lse[row] = (L > 0.f) ? (M + __log2f(L)) * kLn2 : -INFINITY;
+                        p.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
                 }
                 bt += nb;
                 continue;
@@ -1073,7 +1080,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (!ok)
                     break;
                 tc_fence_after();
-                const float inv_l = (l > 0.f) ? p.o_scale / l : 0.f;
+                const float inv_l = l == 0.f ? 0.f : p.o_scale / l;
 #pragma unroll 1
                 for (int c0 = 0; c0 < p.d_io; c0 += 32) {
                     uint32_t o[32];
@@ -1120,9 +1127,9 @@ __global__ void __launch_bounds__(384, 1)
                 tc_fence_before();
                 if (partial) {
                     if (row_valid)
-                        p.part_lse[part_row()] = (l > 0.f) ? m_ref + __log2f(l) : -INFINITY;
+                        p.part_lse[part_row()] = l == 0.f ? -INFINITY : m_ref + __log2f(l);
                 } else if (row_valid && p.lse) {
-                    p.lse[row] = (l > 0.f) ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
+                    p.lse[row] = l == 0.f ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
                 }
             } else if (partial) {
                 // no key of this share for any row of the tile: its partial carries no weight
@@ -1184,7 +1191,8 @@ __global__ void __launch_bounds__(128) fwd_combine_kernel(FwdParams p)
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    const float wl = (M != -INFINITY && ls != -INFINITY) ? ex2_approx(ls - M) : 0.f;
+    // (M leaves out shares that are NaN: their weight is NaN, and so is the row)
+    const float wl = ls == -INFINITY ? 0.f : ex2_approx(ls - (M == -INFINITY ? 0.f : M));
     float L = wl;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
@@ -1239,7 +1247,7 @@ __global__ void __launch_bounds__(128) fwd_combine_kernel(FwdParams p)
                     acc[k] = fmaf(w[j], v[j][k], acc[k]);
         }
     }
-    const float inv = (L > 0.f) ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     T* o = static_cast<T*>(p.o) + (size_t)row * p.d_io + (size_t)n * lane;
     if (n == 4) {
         *reinterpret_cast<uint2*>(o) = make_uint2(Elt<T>::pack(acc[0] * inv, acc[1] * inv),
@@ -1256,7 +1264,7 @@ __global__ void __launch_bounds__(128) fwd_combine_kernel(FwdParams p)
                 o[k] = Elt<T>::from_float(acc[k] * inv);
     }
     if (lane == 0 && p.lse)
-        p.lse[row] = (L > 0.f) ? (M + __log2f(L)) * kLn2 : -INFINITY;
+        p.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
 }
 
 }  // namespace fa

@@ -502,9 +502,24 @@ __device__ __forceinline__ float fmax3(float a, float b, float c)
     return d;
 }
 
+// Maxima that are NaN where an argument is (at the rate of those that drop it).
+__device__ __forceinline__ float fmax_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // 2^x on the FMA pipe, two values at a time, for x >= -125 (smaller x is clamped
-// to -125, i.e. gives about 2.4e-38 instead of 0; callers keep masked -inf scores
-// on the ex2.approx path).  Cody-Waite style reduction x = n + f with
+// to -125, i.e. gives about 2.4e-38 instead of 0; so does a NaN: callers keep masked
+// -inf scores on the ex2.approx path and look for NaN themselves).  Cody-Waite style reduction x = n + f with
 // n = round-to-nearest(x) (add and subtract 1.5 * 2^23) and f in [-1/2, 1/2]; 2^f
 // from the degree-4 polynomial interpolating 2^f at the five Chebyshev nodes of
 // [-1/2, 1/2] (coefficients computed in double and rounded to float; maximum

@@ -32,6 +32,8 @@
  *    j <= i + (Nk - Nq) (the mask is aligned to the bottom-right corner; for
  *    Nq = Nk this is the usual lower triangle).  A query row that sees no key
  *    gets O = 0, LSE = -inf and zero gradients.
+ *    A NaN in a row's query or in a key it sees, or a score that overflows to +inf, makes its
+ *    O and LSE NaN, however its keys are cut between thread blocks; a score of -inf takes no weight.
  *  - stream is a cudaStream_t (NULL = the legacy default stream).  All work is
  *    enqueued on it; no call synchronises the stream or the device.  A call's
  *    first kernel is a plain launch: it starts after all earlier work on the
