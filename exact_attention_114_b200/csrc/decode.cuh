@@ -313,16 +313,16 @@ __global__ void __launch_bounds__(160, 2)   // two CTAs per SM (shared memory al
         float M = -INFINITY;
         for (int w = 0; w < 4; ++w)
             M = fmaxf(M, sm_m[w * 16 + r]);
+        const float base = M == -INFINITY ? 0.f : M;   // a row without keys: l = 0, o = 0 (or l is NaN)
         float L = 0.f, acc = 0.f;
-        if (M != -INFINITY) {
-            for (int w = 0; w < 4; ++w) {
-                const float sc = ex2_approx(sm_m[w * 16 + r] - M);
-                L += sm_l[w * 16 + r] * sc;
-                acc += sm_o[(w * 16 + r) * 128 + dcol] * sc;
-            }
+        for (int w = 0; w < 4; ++w) {
+            const float sc = ex2_approx(sm_m[w * 16 + r] - base);
+            L += sm_l[w * 16 + r] * sc;
+            acc += sm_o[(w * 16 + r) * 128 + dcol] * sc;
         }
-        const float on = (L > 0.f) ? acc / L : 0.f;
-        const float lse = (L > 0.f) ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
+        // 0 and -inf only for a row without keys; a NaN L stays one, in a partial too
+        const float on = L == 0.f ? 0.f : acc / L;
+        const float lse = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994530942f;
         if (p.splits == 1) {
             const int h = hk * p.G + r / p.Nq, i = r % p.Nq;
             const size_t row = ((size_t)b * p.Hq + h) * p.Nq + i;
@@ -361,20 +361,19 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(DecodeParams p)
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     float L = 0.f;
-    if (M != -INFINITY) {
-        for (int s = 0; s < p.splits; ++s) {
-            const size_t prow = base + (size_t)s * p.R;
-            const float ls = p.part_lse[prow];
-            const float w = __expf(ls - M);
-            L += w;
-            const float4 v = *reinterpret_cast<const float4*>(p.part_o + prow * 128 + lane * 4);
-            acc[0] += w * v.x;
-            acc[1] += w * v.y;
-            acc[2] += w * v.z;
-            acc[3] += w * v.w;
-        }
+    const float ref = M == -INFINITY ? 0.f : M;   // (M leaves out splits that are NaN: their w is NaN)
+    for (int s = 0; s < p.splits; ++s) {
+        const size_t prow = base + (size_t)s * p.R;
+        const float ls = p.part_lse[prow];
+        const float w = __expf(ls - ref);
+        L += w;
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + prow * 128 + lane * 4);
+        acc[0] += w * v.x;
+        acc[1] += w * v.y;
+        acc[2] += w * v.z;
+        acc[3] += w * v.w;
     }
-    const float inv = (L > 0.f) ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     const int h = hk * p.G + r / p.Nq, i = r % p.Nq;
     const size_t row = ((size_t)b * p.Hq + h) * p.Nq + i;
     uint2 w2;
@@ -383,7 +382,7 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(DecodeParams p)
     if (lane * 4 < p.d_io)
         *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + row * p.d_io + lane * 4) = w2;
     if (lane == 0 && p.lse)
-        p.lse[row] = (L > 0.f) ? M + __logf(L) : -INFINITY;
+        p.lse[row] = L == 0.f ? -INFINITY : M + __logf(L);
 }
 
 }  // namespace fa

@@ -194,3 +194,27 @@ def test_gradients():
     for g in (dk, dv):
         assert torch.isnan(g[0, 0, :4]).all() and torch.isnan(g[0, 0, 300:]).all()
     assert torch.isfinite(dv[0, 0, 4:128]).all() and torch.isfinite(dq[0, 0]).all()
+
+
+@pytest.mark.parametrize("case", [(2, 8, 2, 1, 60, 128, False), (2, 8, 2, 1, 9000, 128, False), (1, 4, 1, 4, 5000, 64, True), (1, 2, 2, 2, 33000, 96, True)],
+                         ids=str)
+def test_dense_decode(case):
+    """The split-KV decode of the plain forward: one split, and several merged."""
+    B, Hq, Hkv, Nq, Nk, d, causal = case
+    q, k, v, _ = make(B, Hq, Hkv, Nq, Nk, d, BF16, 4800)
+    seen = window_seen(Nq, Nk, Nk, 0, "cuda") if causal else torch.ones(Nq, Nk, dtype=torch.bool, device="cuda")
+    poison(lambda q, k: fa.fa_fwd(q, k, v, causal=causal), q, k, seen, [0, Nk // 2, Nk // 2 + 1, Nk - 1])
+
+
+@pytest.mark.parametrize("lens", [[60], [9000, 8000], [640, 300, 5000]])
+def test_dense_paged_decode(lens):
+    B, Hq, Hkv, d, n = len(lens), 8, 2, 128, lens[0]
+    q, k, v, _ = make(B, Hq, Hkv, 1, -(-max(lens) // 64) * 64, d, FP16, 4900)
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+    def call(q, k):
+        table = torch.arange(B * k.shape[2] // 64, dtype=torch.int32, device="cuda").view(B, -1)
+        pool = lambda t: t.transpose(1, 2).reshape(-1, 64, Hkv, d).contiguous()  # noqa: E731
+        return fa.fa_fwd_paged(q, pool(k), pool(v), table, ln)
+
+    poison(call, q, k, torch.ones(1, n, dtype=torch.bool, device="cuda"), [0, n // 2, n - 1])
