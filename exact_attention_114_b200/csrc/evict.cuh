@@ -11,6 +11,7 @@
 //   evict_gather_kernel    their rows of K and V, moved to the front of a new cache
 #pragma once
 
+#include <climits>
 #include <type_traits>
 
 #include "sm100.cuh"
@@ -34,15 +35,17 @@ struct KeyWeightParams {
 
 // 2^x for both lanes on the FMA pipe: x = n + f, f in [-1/2, 1/2], times the degree-5 polynomial
 // through 2^f at the six Chebyshev nodes cos((2 k + 1) pi / 12) / 2 (relative error 2.4e-7; the
-// degree-4 one of the forward has 3.6e-6, which sums of weights in fp32 would show).
+// degree-4 one of the forward has 3.6e-6, which sums of weights in fp32 would show).  2^n is a factor
+// of its own, bits (n + 127) << 23: 0 for n = -127, at which x is held (so what lies below -126.5 is 0,
+// -inf too), and a NaN x stays NaN.
 constexpr float kKeyExp2C0 = 1.0000001192092896f, kKeyExp2C1 = 0.69314718246459961f,
                 kKeyExp2C2 = 0.24022106826305389f, kKeyExp2C3 = 0.055503569543361664f,
                 kKeyExp2C4 = 0.009676031768321991f, kKeyExp2C5 = 0.0013390863314270973f;
 
 __device__ __forceinline__ float2 key_weight_exp2(float2 x)
 {
-    x.x = fmaxf(x.x, -125.f);
-    x.y = fmaxf(x.y, -125.f);
+    x.x = fmax_nan(x.x, -127.f);
+    x.y = fmax_nan(x.y, -127.f);
     const float2 t = fadd2(x, make_float2(12582912.f, 12582912.f));
     const float2 f = fadd2(x, fadd2(make_float2(12582912.f, 12582912.f), make_float2(-t.x, -t.y)));
     float2 q = ffma2(make_float2(kKeyExp2C5, kKeyExp2C5), f, make_float2(kKeyExp2C4, kKeyExp2C4));
@@ -50,8 +53,8 @@ __device__ __forceinline__ float2 key_weight_exp2(float2 x)
     q = ffma2(q, f, make_float2(kKeyExp2C2, kKeyExp2C2));
     q = ffma2(q, f, make_float2(kKeyExp2C1, kKeyExp2C1));
     q = ffma2(q, f, make_float2(kKeyExp2C0, kKeyExp2C0));
-    return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(t.x) << 23)),
-                       __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
+    return fmul2(q, make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3F800000),
+                                __int_as_float((__float_as_int(t.y) << 23) + 0x3F800000)));
 }
 
 // pairs in four whose exponentials go to the FMA pipe
@@ -224,8 +227,7 @@ __global__ void __launch_bounds__(KeyWCfg<D>::kThreads, KeyWCfg<D>::kCtas)
             th = kvh * p.heads + (it_lo + g) / nqb;
             qb = (it_lo + g) % nqb;
         }
-        // LSE of this thread's row of the next step (loaded a step ahead); rows past the last count as
-        // seeing no key
+        // LSE of this thread's row of the next step (loaded a step ahead)
         auto next_lse = [&](int it) {
             const int row = (qb0 + qb) * 128 + c0;
             return it < n_it && row < p.rows ? __ldg(p.lse + (size_t)th * p.rows + row) : -INFINITY;
@@ -241,8 +243,10 @@ __global__ void __launch_bounds__(KeyWCfg<D>::kThreads, KeyWCfg<D>::kCtas)
             float* v = vec + (u & 1) * 128;
             int* ps = pos + (u & 1) * 128;
             v[c0] = nl;
-            if (p.causal)
-                ps[c0] = (p.rows == p.Nq ? row : row % p.Nq) + delta;
+            // the last step of a head may end past its rows: those see nothing (32 of them at a time are left out)
+            const int n_rows = p.rows - row0;
+            if (p.causal || n_rows < 128)
+                ps[c0] = row >= p.rows ? INT_MIN : !p.causal ? INT_MAX : (p.rows == p.Nq ? row : row % p.Nq) + delta;
             // (nobody still reads the buffer of two steps ago; the four warps go on or stop together)
             ok = named_bar_and(1 + g, 128, ok);
             if (!ok)
@@ -268,7 +272,9 @@ __global__ void __launch_bounds__(KeyWCfg<D>::kThreads, KeyWCfg<D>::kCtas)
                     if (lane == 0)
                         mbar_arrive(&bar_free[b]);
                 }
-                if (!masked) {
+                if (32 * h >= n_rows)
+                    continue;
+                if (!masked && 32 * h + 32 <= n_rows) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 8) {
                         const float4 n0 = v4[8 * h + (c >> 2)], n1 = v4[8 * h + (c >> 2) + 1];

@@ -183,6 +183,47 @@ def test_weights_of_single_tokens(shape, causal):
     assert torch.isnan(w[bad]).all() and torch.equal(w[~bad], w0[~bad])
 
 
+PROMPTS = [
+    # B, Hq, Hkv, Nq, Nk, d, causal: many rows, the last step of a head full or not, a group's rows as one run
+    (1, 2, 1, 300, 300, 128, True), (1, 2, 1, 300, 700, 64, False), (1, 2, 2, 256, 513, 128, False), (2, 8, 2, 20, 300, 64, True),
+    (1, 2, 1, 200, 300, 256, False), (1, 16, 1, 1100, 1100, 64, True),
+]
+
+
+@pytest.mark.parametrize("case", PROMPTS, ids=str)
+def test_weights_of_prompts(case):
+    """A NaN query row shows in the weights of every key it sees, whatever its index, and in no other."""
+    B, Hq, Hkv, Nq, Nk, d, causal = case
+    q, k, v, _ = make(B, Hq, Hkv, Nq, Nk, d, BF16, 4650)
+    seen = window_seen(Nq, Nk, Nk, 0, "cuda") if causal else torch.ones(Nq, Nk, dtype=torch.bool, device="cuda")
+    w0 = fa.fa_fwd_weights(q, k, v, causal=causal)[2]
+    assert torch.isfinite(w0).all()
+    for i in eights(0, Nq - 8):
+        q2 = q.clone()
+        q2[0, Hq - 1, i, 1] = math.nan
+        w = fa.fa_fwd_weights(q2, k, v, causal=causal)[2]
+        bad = torch.zeros_like(w, dtype=torch.bool)
+        bad[0, Hkv - 1] = seen[i]
+        assert torch.isnan(w[bad]).all() and torch.equal(w[~bad], w0[~bad])
+
+
+@pytest.mark.parametrize("Nq", [256, 300, 100, 1])
+def test_weights_that_vanish_are_zero(Nq):
+    """Keys whose scores lie 100 below the others': exp underflows, the weight is 0 and not a small number; and a
+    key with an infinite column, whose scores are all -inf, gets 0 too (rows past the last have no say)."""
+    q, k, v, _ = make(1, 2, 1, Nq, 700, 64, BF16, 4660)
+    q[..., 0], k[..., 0] = 8.0, 0.0
+    k[:, :, 100:140] = 0.0
+    k[:, :, 100:140, 0] = -130.0
+    k[:, :, 300, 0] = -math.inf
+    o, lse, w = fa.fa_fwd_weights(q, k, v)
+    again = fa.fa_key_weights(q, k, lse)
+    torch.cuda.synchronize()
+    for x in (w, again):
+        assert not x[:, :, 100:140].any() and not x[:, :, 300].any() and torch.isfinite(x).all()
+        assert abs(float(x.double().sum()) - 2 * Nq) <= 2 * Nq * 1e-4
+
+
 def test_gradients():
     """A NaN query row: its own gradient, and those of the keys it sees, are NaN, not numbers."""
     q, k, v, dout = make(1, 2, 1, 400, 400, 128, BF16, 4700)

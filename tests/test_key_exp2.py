@@ -36,3 +36,28 @@ def test_relative_error():
     # interpolation 1.1e-7 (absolute, so at most 1.6e-7 relative), Horner's last two roundings 2 x 2^-24
     # each of values up to sqrt(2) on results from 1 / sqrt(2), and the rounded coefficients: below 5e-7
     assert np.abs(y / np.exp2(x.astype(np.float64)) - 1.0).max() <= 5e-7
+
+
+def as_the_kernel(x):
+    """fp32 Horner after the split, 2^n as a factor (n + 127) << 23; x held at -127, a NaN kept."""
+    c, magic = coefficients(), np.float32(12582912.0)
+    x = np.where(np.isnan(x), x, np.maximum(x, np.float32(-127.0))).astype(np.float32)
+    t = (x + magic).astype(np.float32)
+    f = (x - (t - magic).astype(np.float32)).astype(np.float32)
+    q = c[5]
+    for k in range(4, -1, -1):
+        q = (q * f + c[k]).astype(np.float32)
+    return q * ((t.view(np.int32) << 23) + np.int32(0x3F800000)).astype(np.int32).view(np.float32)
+
+
+def test_below_the_smallest_normal_and_not_a_number():
+    y = as_the_kernel(np.array([-np.inf, -1e30, -1000.0, -127.0, -126.51], np.float32))
+    assert not y.any()
+    assert np.isnan(as_the_kernel(np.array([np.nan], np.float32))).all()
+    x = np.linspace(-126.0, 1.0, 1_000_001).astype(np.float32)
+    y = as_the_kernel(x).astype(np.float64)
+    normal = x >= -125.5   # (below, a result may be under 2^-126, which the GPU may take for 0)
+    assert np.abs(y / np.exp2(x.astype(np.float64)) - 1.0)[normal].max() <= 5e-7
+    # the source holds x at the same place and keeps a NaN
+    text = open(SRC, encoding="utf-8").read()
+    assert text.count("fmax_nan(x.x, -127.f)") == 1 and text.count("fmax_nan(x.y, -127.f)") == 1
