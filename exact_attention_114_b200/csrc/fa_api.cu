@@ -2317,11 +2317,18 @@ fa_status_t fa_bwd_ex(fa_dtype_t dtype, const void* q, const void* k, const void
                      workspace, workspace_bytes, stream);
 }
 
-// Whether a size query's sizes are ones that the call would take (no error is recorded).
-static bool sizes_ok(int B, int Hq, int Hkv, int Nq, int Nk, int d)
+// Whether a size query's sizes are ones that the call would take.  The thread's last error stays as it
+// was, and no exception passes.
+static bool sizes_ok(int B, int Hq, int Hkv, int Nq, int Nk, int d) noexcept
 {
-    const bool ok = check_shape(B, Hq, Hkv, Nq, Nk, d, 1.f, 0) == FA_OK;
-    t_error.clear();
+    std::string last;
+    last.swap(t_error);
+    bool ok = false;
+    try {
+        ok = check_shape(B, Hq, Hkv, Nq, Nk, d, 1.f, 0) == FA_OK;
+    } catch (...) {
+    }
+    t_error.swap(last);
     return ok;
 }
 

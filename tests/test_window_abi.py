@@ -76,6 +76,18 @@ def test_paged_refuses():
     assert fa.fa_fwd_paged_window_workspace_size(2, 8, 2, 1, 64, 20, 128, 0, 4) == 0
 
 
+def test_size_queries_leave_the_last_error():
+    assert fwd(window=0) == fa.FA_ERR_INVALID_ARGUMENT
+    message = fa.last_error_message()
+    assert "window=0" in message
+    for B in (1, 0):   # sizes that the calls take, and sizes that they refuse
+        fa.fa_bwd_window_workspace_size(B, 2, 1, 300, 300, 64, 10, 4)
+        fa.fa_bwd_window_query_split(B, 2, 1, 300, 300, 64, 10, 4)
+        fa.fa_fwd_paged_window_workspace_size(B, 8, 2, 1, 64, 20, 128, 500, 4)
+        fa.fa_fwd_prefix_workspace_size(B, 8, 2, 1, 500, 64, 128)
+        assert fa.last_error_message() == message
+
+
 def test_binding_refuses():
     x = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
