@@ -464,8 +464,9 @@ def _scale(scale, d):
 
 
 def _keys(n):
-    """A number of keys as the C call's int: more than any cache holds stays the largest (not a remainder)."""
-    return min(int(n), 0x7FFFFFFF)
+    """A number of keys as the C call's int: more than any cache holds stays the largest, less than none
+    stays negative (neither a remainder)."""
+    return max(-1, min(int(n), 0x7FFFFFFF))
 
 
 def _qkv(q, k, v):

@@ -94,3 +94,14 @@ def test_binding_refuses():
         fa.fa_fwd_window(x, x, x, 3)
     with pytest.raises(ValueError, match="dtype"):
         fa.fa_fwd_window(x.float(), x.float(), x.float(), 3)
+
+
+def test_numbers_of_keys_that_do_not_fit_an_int():
+    """Far below zero is refused as negative, not taken for its remainder; far above is the largest."""
+    size, split = fa.fa_bwd_window_workspace_size, fa.fa_bwd_window_query_split
+    shape = (1, 2, 1, 300, 300, 64)
+    for n in (-1, -2 ** 31 - 5, -2 ** 32 + 10, -2 ** 40):
+        assert size(*shape, n) == 0 and size(*shape, 10, n) == 0 and split(*shape, n) == (0, 0)
+        assert fa.fa_fwd_paged_window_workspace_size(2, 8, 2, 1, 64, 20, 128, n, 4) == 0
+    for n in (300, 2 ** 31, 2 ** 32 + 10, 2 ** 40):
+        assert size(*shape, n, n) == size(*shape, 300, 300) > 0
