@@ -1242,7 +1242,9 @@ fa_status_t run_stream(const StreamArgs& a, void* workspace, size_t workspace_by
 // ---------------------------------------------------------------------------
 // forward of a batch whose sequences share a prefix
 // ---------------------------------------------------------------------------
-constexpr long long kPrefixUnpackedTiles = 4096;
+constexpr long long kPrefixUnpackedTiles = 4096;        // of 64 keys: split-KV pass
+constexpr long long kPrefixUnpackedTilesTiled = 2048;   // tiled pass
+constexpr int kPrefixUnpackedKeysTiled = 32768;
 
 struct PrefixArgs {
     const void *q, *kp, *vp, *k, *v;
@@ -1255,15 +1257,26 @@ struct PrefixArgs {
 };
 
 // Rows of several sequences fit a 128-row tile: the prefix in a pass of its own, which reads it
-// once for all of them, and a merge.  Where a sequence's rows fill half a tile or more, packing
-// saves nothing, and one launch reads the prefix and then the own keys.  So it does for a batch and
-// prefix so small that reading the prefix once per sequence (from L2, in the split-KV pass) is
-// quicker than a pass and a merge more: up to 4096 tiles of 64 keys.
+// once for all of them, and a merge.  A tile holds whole sequences, so beyond 64 rows it would hold
+// one, and one launch reads the prefix and then the own keys.  So it does for a batch and prefix so
+// small that reading the prefix once per sequence (mostly from L2) is quicker than a pass and a merge
+// more.  Per sequence against packed, 32 / 8 heads, own keys 128, us:
+//   single tokens (split-KV pass), d = 128, by B * Hkv * prefix tiles of 64 keys: 1024 tiles 22 - 26
+//   against 24 - 34, 2048 tiles 22 - 28 against 25 - 36, 4096 tiles 28 - 34 against 26 - 38, 8192 tiles
+//   38 - 44 against 30 - 38, 16384 tiles 59 - 65 against 32 - 38 (two sequences: 73 against 75)
+//   20 to 64 rows (tiled pass): one block of prefix 14 against 26 - 32; 2048 tiles 30 - 37 against
+//   32 - 69, 4096 tiles 37 - 47 against 36 - 73, 8192 tiles 59 - 72 against 42 - 81; d = 256, 2048 tiles
+//   31 - 47 against 35 - 110, 4096 tiles 45 - 63 against 38 - 115
+// A unit is cut into at most 32 shares, so that one launch is the slower one for few units of very long
+// keys: 2 sequences of one kv head on 65536 keys, 65 against 50 (on 32768: 41 both).
 bool prefix_packs(const PrefixArgs& a)
 {
     if (a.B == 1 || 2LL * (a.Hq / a.Hkv) * a.Nq > 128)
         return false;
-    return !decode_shape(a.Hq, a.Hkv, a.Nq, a.d) || (long long)a.B * a.Hkv * ((a.Np + 63) / 64) > kPrefixUnpackedTiles;
+    const long long tiles = (long long)a.B * a.Hkv * ((a.Np + 63) / 64);
+    if (decode_shape(a.Hq, a.Hkv, a.Nq, a.d))
+        return tiles > kPrefixUnpackedTiles;
+    return tiles > kPrefixUnpackedTilesTiled || a.Np > kPrefixUnpackedKeysTiled;
 }
 
 // 4-D map over q as [B][Hkv][rows][d], box {64, rows, 1, pack}: a kv head's rows of `pack` sequences

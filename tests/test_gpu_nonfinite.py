@@ -89,6 +89,7 @@ PREFIX = [
     # launch (whole, cut, cluster)
     (3, 8, 2, 1, 500, 70, 128), (2, 8, 2, 1, 9000, 200, 128), (70, 16, 8, 1, 1030, 140, 64), (4, 8, 2, 9, 1500, 300, 128),
     (4, 4, 2, 64, 500, 200, 128), (1, 2, 1, 200, 5000, 300, 256), (2, 4, 2, 128, 2000, 500, 128), (40, 8, 2, 40, 300, 200, 96),
+    (40, 8, 4, 9, 900, 129, 128), (75, 8, 2, 1, 1100, 77, 256),
 ]
 
 

@@ -139,3 +139,28 @@ def test_graph_streams_and_repeats(Nq, Np):
     fa.fa_check_device_status()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert all(torch.equal(o, want[0]) and torch.equal(l, want[1]) for o, l in outs)
+
+
+PACKED = [
+    # rows of several sequences in a tile and the tiled pass for the own keys: prefixes too long to be read per sequence
+    (40, 8, 4, 9, 900, 129, 128, [(17 * i) % 130 for i in range(40)]), (90, 2, 1, 32, 1600, 100, 64, [100 - i for i in range(90)]),
+    (75, 8, 2, 1, 1100, 77, 256, [i % 78 for i in range(75)]), (70, 4, 2, 5, 1090, 40, 160, [i % 41 for i in range(70)]),
+    (3, 6, 1, 3, 33000, 70, 96, [70, 0, 33]), (2, 32, 1, 2, 33000, 100, 128, None), (129, 2, 2, 64, 520, 65, 32, [0] * 128 + [65]),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("case", PACKED, ids=lambda c: str(c[:7]))
+def test_packed_tiled_prefix(case, causal, dtype):
+    *shape, lens = case
+    assert fa.fa_fwd_prefix_workspace_size(*shape) > 0   # partials of the prefix pass
+    q, kp, vp, k, v = make_prefix(*shape, dtype, 3500 + PACKED.index(case))
+    if lens is not None:
+        for b, n in enumerate(lens):
+            k[b, :, n:], v[b, :, n:] = math.nan, math.inf
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = fa.fa_fwd_prefix(q, kp, vp, k, v, ln, causal=causal)
+    torch.cuda.synchronize()
+    fa.fa_check_device_status()
+    check(q, kp, vp, k, v, lens, causal, o, lse)

@@ -34,6 +34,17 @@ def test_workspace_sizes():
     assert fa.fa_fwd_prefix_workspace_size(4, 8, 2, 1, 0, 64, 128) == 0
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,Np,d,packs", [
+    (8, 32, 8, 5, 128, 128, False), (8, 32, 8, 5, 2048, 128, False), (8, 32, 8, 5, 2049, 128, True), (2, 4, 1, 9, 32768, 128, False),
+    (2, 4, 1, 9, 32769, 128, True), (2, 4, 1, 1, 200, 256, False), (64, 32, 8, 1, 300, 256, True), (1, 4, 1, 9, 90000, 128, False),
+    (64, 32, 8, 17, 4096, 128, False),
+])
+def test_short_prefixes_are_read_per_sequence(B, Hq, Hkv, Nq, Np, d, packs):
+    """More rows than the split-KV pass takes: up to 2048 tiles of 64 keys over the batch's kv heads (and 32768
+    keys) one launch without partials of its own, beyond that the prefix in a pass of its own."""
+    assert (fa.fa_fwd_prefix_workspace_size(B, Hq, Hkv, Nq, Np, 100, d) > 0) == packs
+
+
 def test_binding_refuses():
     x, p = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 9, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
