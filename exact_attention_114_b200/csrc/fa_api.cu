@@ -676,9 +676,12 @@ fa_status_t check_window(int window, int sinks, int Nk, Window* w)
 
 // Two shares of every work tile as a cluster of two CTAs (no partials through memory): where that
 // takes no more CTAs than SMs and less time than the plan `sp` of shares merged by a kernel.  In block
-// times of the longest tile, plus 3 for the plan's merge kernel and 1.5 for a pair's exchange (as
-// measured: 512 rows on 16K keys 53.9 us merged by the kernel, 47.6 as pairs; 40 rows on 5K keys, whose
-// 2 tiles take 8 shares each, 18.9 against 26.7).
+// times of the longest tile, plus 3 for the plan's merge kernel and 1.5 for a pair's exchange.  Plan
+// against pairs, us, the taken one first: pairs for 512 rows on 16K keys, window 4096, 32 heads (53
+// against 61), 1024 rows on 4K, window 1024, 16 heads (31, 35), 512 on 2K, 16 heads (29, 33), 256 on
+// 1500, 32 heads (29, 33), 64 rows of 4 heads on a prefix of 4096, 64 units (51, 59); the plan for 256 on
+// 16K, window 4096, 32 heads (40, 51), the same with 8 heads (32, 49), 257 on 3000, 8 heads (26, 29),
+// 40 rows on 5000 (20, 27), 16 units on a prefix of 4096 (32, 49).
 bool fwd_pairs(const FwdGeom& g, int tiles_per_cta, int longest, const FwdSplit& sp, int sms)
 {
     const long long units = (long long)g.n_pairs * g.n_bh;
@@ -1793,7 +1796,10 @@ fa_status_t check_weights(const float* in, const float* out, size_t n)
     return FA_OK;
 }
 
-// Kept rows of K and V of a (batch, kv head) up to which the selecting block moves them itself.
+// Kept rows of K and V of a (batch, kv head) up to which the selecting block moves them itself.  Itself
+// against a gather kernel, a quarter of the keys kept, us: 16 KB 12 against 14 (2 to 32 caches) and 14
+// against 16 (128), 64 KB 14 - 18 against 16 - 20, 128 KB 16 - 20 against 16 - 22, 256 KB 20 - 29 against
+// 18 - 29.
 constexpr size_t kEvictFusedBytes = 128 * 1024;
 
 // No exception (host memory) passes a C entry.
