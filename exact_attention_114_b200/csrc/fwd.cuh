@@ -889,7 +889,7 @@ __global__ void __launch_bounds__(384, 1)
                 // (a NaN block is taken too: it makes l and O NaN, and so do the blocks after a NaN reference)
                 if (!(m_blk <= m_ref + kRescaleLog2)) {
                     a = ex2_approx(m_ref - m_blk);
-                    resc = (j > 0);
+                    resc = (j > 0) && in_pack;   // (rows of a packed tile that hold no query may hold anything)
                     m_ref = m_blk;
                     l *= a;
                 }
