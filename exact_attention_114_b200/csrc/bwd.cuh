@@ -3,6 +3,10 @@
 // statistic instead of reading a stored P).  For L = sum(dO * O):
 //   P = exp(scale q.k - LSE),  dV += P^T dO,  dP = dO V^T,  D = rowsum(dO * O),
 //   dS = P * (dP - D),  dK += scale dS^T Q,  dQ += scale dS K.
+// P and dS are rounded to the 16-bit type as operands of the matrix products, half a step each, about
+// what rounding the gradients themselves costs (relative error 1.4 of that alone).  D is taken from the
+// 16-bit O, the only one that the caller has: under short windows, where O is large beside dP, that
+// makes 1.5 of it in dQ and dK.  Sums, D and the dQ accumulator are fp32.
 //
 // Three kernels:
 //   bwd_pre   one warp per query row: D_i, LSE_i * log2(e) (+inf for rows that
@@ -29,7 +33,8 @@
 // shares those would run on after the others (at 8192 rows, window 1024, one sinks' unit is 6.5
 // others), so the launch has two parts, each with its own number of CTAs per unit.  Same
 // bound as the dense kernel (tensor and shared memory), over blocks of 1.2 times the visible
-// pairs: 460 us of the 525 us backward at that shape with 32 / 8 heads, d = 128.
+// pairs: 436 us of the 535 us backward at that shape with 32 / 8 heads, d = 128, at 1965 MHz (574 at
+// the 1.7 GHz of a loop at the power limit).
 //
 // bwd_main roles (384 threads = 3 warpgroups):
 //   warps 0-3  thread r = key r = TMEM lane r: read S^T and dP^T rows from TMEM,

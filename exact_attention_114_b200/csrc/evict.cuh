@@ -85,8 +85,9 @@ struct KeyWCfg {
 // key r, so a step's sum over rows is a sum over the thread's own registers, and no two threads ever
 // add to the same key.  The exponentials bound it (128 x 128 of them against 2 x 128 x 128 x d flops): one pair in four goes to the FMA pipe, and
 // four warps per scheduler keep both pipes fed across the waits for TMEM and barriers.  GQA 32 / 8,
-// 4096 rows, d = 128, causal: 96 us (without the mask 160 us: 3.3e12 exponentials a second, 0.75 of the
-// MUFU's own rate).
+// 4096 rows, d = 128, causal: 89 us (without the mask 165 us: 3.3e12 exponentials a second, 0.75 of the
+// MUFU's own rate; with the mask a CTA has 1 to 32 steps, each with the same set-up); 95 behind a forward
+// in a loop at the power limit.
 template <int D, typename T>
 __global__ void __launch_bounds__(KeyWCfg<D>::kThreads, KeyWCfg<D>::kCtas)
     key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,

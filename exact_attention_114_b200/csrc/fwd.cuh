@@ -53,8 +53,9 @@
 //     row.  The block where the two meet is two TMA boxes.  A window starts and
 //     ends inside a block for most rows, so the masks are visible columns as bits,
 //     and only for warps with a row that needs one (8192 rows, window 1024, 4 sinks,
-//     32 heads, d = 128: 174 us, 743 TFLOP/s over the visible pairs; compared
-//     element by element 274 us).  Bound by the tensor pipe and the exponentials,
+//     32 heads, d = 128: 172 - 185 us at 1965 MHz, 700 - 750 TFLOP/s over the visible
+//     pairs, 199 at the 1.7 GHz of a loop at the power limit; compared element by
+//     element 274 us).  Bound by the tensor pipe and the exponentials,
 //     over blocks of 1.3 times the visible pairs.
 //   * kFwdCat (shared prefix): the prefix's blocks, then the sequence's own.
 //   * kFwdPack (shared prefix): the prefix's blocks for a tile that holds the rows of

@@ -384,12 +384,18 @@ fa_status_t fa_fwd_paged_window(fa_dtype_t dtype, const void* q, const void* k_c
  *   Np + seq_lens[b] keys (bottom-right, as above; with fewer own keys than rows
  *   the first rows lie inside the prefix).
  * The result is that of fa_fwd_ex on the concatenated keys.  Where several
- * sequences' rows (Nq * Hq / Hkv each) fit a tile of 128, the prefix is read and
- * multiplied once for all of them, the own keys by the split-KV or the tiled
- * kernel, and the partial results merged as blocks are (§04); otherwise one
- * launch walks the prefix and then the own keys.
- *   workspace: fa_fwd_prefix_workspace_size() bytes (0 where no partials are
- *   merged), 256-byte aligned, or NULL (allocated stream-ordered).
+ * sequences' rows (Nq * Hq / Hkv each) fit a tile of 128 and the prefix is long,
+ * the prefix is read and multiplied once for all of them, the own keys by the
+ * split-KV or the tiled kernel, and the partial results merged as blocks are
+ * (§04).  Otherwise one pass walks the prefix and then the own keys of each
+ * sequence: for rows that fill half a tile or more, and for prefixes of up to
+ * 4096 tiles of 64 keys over the batch's B * Hkv kv heads in decode shapes, 2048
+ * (and 32768 keys) in others, which stay in L2.
+ *   workspace: fa_fwd_prefix_workspace_size() bytes, 256-byte aligned, or NULL
+ *   (allocated stream-ordered).  The size is 0 where the tiled kernel walks all
+ *   keys in one pass; where that pass cuts its tiles into key shares, their
+ *   partials are stream-ordered scratch of the call's own, as in fa_fwd_ex, with a
+ *   workspace too.
  */
 size_t fa_fwd_prefix_workspace_size(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d);
 fa_status_t fa_fwd_prefix(fa_dtype_t dtype, const void* q, const void* k_prefix, const void* v_prefix,
