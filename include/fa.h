@@ -411,7 +411,8 @@ fa_status_t fa_fwd_prefix(fa_dtype_t dtype, const void* q, const void* k_prefix,
  *   weights_in, weights_out: [B, Hkv, Nk] fp32; weights_in NULL counts as zeros,
  *   and may be weights_out itself (added up in place) but not overlap it in
  *   another way.  Sums are taken in fp32 in a fixed order (they repeat bitwise).
- *   Rows that see no key (lse = -inf) add nothing.
+ *   Rows that see no key (lse = -inf) add nothing; one whose lse is NaN makes the
+ *   weights of the keys it sees NaN, and of no others.
  * fa_key_weights takes the lse of an earlier forward of the same q, k, scale and
  * causal flag.  fa_fwd_weights is fa_fwd_ex that also adds the weights: in decode
  * shapes (Nq * Hq / Hkv <= 16, d <= 128) the split pass leaves its scores (fp32,
