@@ -260,3 +260,24 @@ def test_dense_paged_decode(lens):
         return fa.fa_fwd_paged(q, pool(k), pool(v), table, ln)
 
     poison(call, q, k, torch.ones(1, n, dtype=torch.bool, device="cuda"), [0, n // 2, n - 1])
+
+
+@pytest.mark.parametrize("Nq,Nk", [(300, 300), (128, 20000)])
+def test_e4m3(Nq, Nk):
+    """The e4m3 forward, whole tiles and key shares: the type's NaN in a query row and in visible keys."""
+    g = torch.Generator(device="cuda").manual_seed(5000)
+    q, k, v = (torch.randn(1, 2, n, 128, generator=g, device="cuda").to(torch.float8_e4m3fn) for n in (Nq, Nk, Nk))
+
+    def call(q, k):
+        return fa.fa_fwd_fp8(q.view(torch.float8_e4m3fn), k.view(torch.float8_e4m3fn), v, 1.0, 1.0, 1.0, causal=True)
+
+    seen = window_seen(Nq, Nk, Nk, 0, "cuda")
+    base = call(q, k)
+    for i in (0, Nq - 1):
+        q2, bad = q.view(torch.uint8).clone(), torch.zeros(1, 2, Nq, dtype=torch.bool, device="cuda")
+        q2[0, 1, i, 3], bad[0, 1, i] = 0x7F, True
+        check_rows(call(q2, k), base, bad)
+    for j in eights(Nk // 2):
+        k2 = k.view(torch.uint8).clone()
+        k2[0, 0, j, 5] = 0x7F
+        check_rows(call(q, k2), base, rows_of(seen, j, 1, 2, 2, 0, 0))
